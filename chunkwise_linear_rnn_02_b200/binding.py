@@ -7,6 +7,7 @@ CUDA tensors, the calls raise instead of computing anything elsewhere.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import re
 
@@ -15,7 +16,8 @@ import torch
 __all__ = [
     "GLAError", "load_library", "library_path", "header_symbols", "status_string", "version",
     "chunk_fwd", "chunk_bwd", "chunk_fwd_logit", "chunk_bwd_logit", "recurrent_step", "gsa_fwd", "gsa_bwd", "gsa_recurrent_step",
-    "device_error", "workspace_bytes",
+    "device_error", "workspace_bytes", "scan_fwd", "scan_bwd", "scan_step", "group_norm_fwd", "group_norm_bwd",
+    "rotary", "rotary_bwd", "rotary_frequencies",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -50,6 +52,14 @@ _SIGNATURES = {
     "gla_msgla_pool_bwd": (_i, [_vp, _vp] + [_i] * 6 + [_vp]),
     "gla_msgla_hold": (_i, [_vp, _vp] + [_i] * 6 + [_vp]),
     "gla_msgla_hold_bwd": (_i, [_vp, _vp] + [_i] * 6 + [_vp]),
+    "gla_scan_fwd": (_i, [_vp] * 6 + [_i] * 6 + [_vp]),
+    "gla_scan_bwd_workspace": (_sz, [_i] * 5),
+    "gla_scan_bwd": (_i, [_vp] * 9 + [_i] * 6 + [_vp, _sz, _vp]),
+    "gla_scan_step": (_i, [_vp] * 4 + [_i] * 5 + [_vp]),
+    "gla_group_norm_fwd": (_i, [_vp] * 5 + [_i] * 7 + [ctypes.c_float, _i, _i, _vp]),
+    "gla_group_norm_bwd_workspace": (_sz, [_i] * 7),
+    "gla_group_norm_bwd": (_i, [_vp] * 9 + [_i] * 7 + [ctypes.c_float, _i, _i, _vp, _sz, _vp]),
+    "gla_rotary": (_i, [_vp] * 6 + [ctypes.c_longlong] + [_i] * 7 + [ctypes.c_float] + [_i] * 5 + [_vp]),
 }
 
 
@@ -339,3 +349,237 @@ def msgla_hold(y, T: int, s: int):
 def msgla_hold_bwd(dout, s: int):
     T = dout.shape[2]
     return _msgla("gla_msgla_hold_bwd", dout, -(-T // s), T, s)
+
+
+# ------------------------------------------------------------------------------------------
+# Operators around the recurrences: the elementwise scan, the norm behind them, rotary positions.
+def _operand(name, t, dtype, shape, device):
+    """Address of a tensor that has to be a contiguous CUDA tensor of this dtype, shape and device; None stays."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape:
+        raise GLAError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.device != device:
+        raise GLAError(f"{name} is on {t.device}, the call runs on {device}: tensors must be CUDA tensors of one device"
+                       if device.type == "cuda" else "tensors must be CUDA tensors: this library has no CPU path")
+    if not t.is_contiguous():
+        raise GLAError("tensors must be contiguous")
+    return t.data_ptr()
+
+
+def _first(t, rank):
+    """Check the tensor that fixes dtype, shape and device; returns (dtype code, device)."""
+    if not t.is_cuda:
+        raise GLAError("tensors must be CUDA tensors: this library has no CPU path")
+    if t.dim() != rank:
+        raise GLAError(f"expected a tensor of {rank} dimensions, got shape {tuple(t.shape)}")
+    return _dtype_code(t), t.device
+
+
+def _enqueue(name, device, *args):
+    """Call an entry point on the current stream of the tensors' device, which need not be the current one."""
+    fn = getattr(load_library(), name)
+    if torch.cuda.current_device() == device.index:
+        code = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if code != 0:
+        raise GLAError(f"{name}: {status_string(code)}")
+
+
+SCAN_KEEP = 64  # tokens between the states that scan_fwd(save_states=True) keeps
+
+
+def scan_fwd(g, x, h0=None, complement: bool = False, output_final_state: bool = True, save_states: bool = False):
+    """Elementwise scan h_t = exp(g_t) h_{t-1} + b_t, b = x or, complement, (1 - exp g) x, over [B,H,T,D].
+
+    Returns (o [B,H,T,D], hT [B,H,D] fp32 or None, hc [B,H,ceil(T/64),D] fp32 or None); hc, the states before
+    tokens 0, 64, ..., is what scan_bwd wants.  A [B,T,C] tensor goes in as [B,1,T,C].
+    """
+    dt, dev = _first(g, 4)
+    B, H, T, D = g.shape
+    gp, xp = _operand("g", g, g.dtype, g.shape, dev), _operand("x", x, g.dtype, g.shape, dev)
+    hp = _operand("h0", h0, torch.float32, (B, H, D), dev)
+    o = torch.empty_like(g)
+    hT = torch.empty(B, H, D, dtype=torch.float32, device=dev) if output_final_state else None
+    hc = torch.empty(B, H, -(-T // SCAN_KEEP), D, dtype=torch.float32, device=dev) if save_states else None
+    _enqueue("gla_scan_fwd", dev, gp, xp, hp, o.data_ptr(), None if hT is None else hT.data_ptr(),
+             None if hc is None else hc.data_ptr(), B, H, T, D, int(complement), dt)
+    return o, hT, hc
+
+
+def scan_bwd(g, x, do, h0=None, dhT=None, hc=None, complement: bool = False, need_dh0: bool = True):
+    """Backward of scan_fwd: returns (dg, dx, dh0 or None).  Without hc the states are recomputed from h0."""
+    dt, dev = _first(g, 4)
+    B, H, T, D = g.shape
+    gp, xp = _operand("g", g, g.dtype, g.shape, dev), _operand("x", x, g.dtype, g.shape, dev)
+    dop = _operand("do", do, g.dtype, g.shape, dev)
+    hp = _operand("h0", h0, torch.float32, (B, H, D), dev)
+    dhp = _operand("dhT", dhT, torch.float32, (B, H, D), dev)
+    hcp = _operand("hc", hc, torch.float32, (B, H, -(-T // SCAN_KEEP), D), dev)
+    dg, dx = torch.empty_like(g), torch.empty_like(g)
+    dh0 = torch.empty(B, H, D, dtype=torch.float32, device=dev) if need_dh0 else None
+    ws, nb = (None, 0)
+    if hc is None:
+        ws, nb = _workspace(load_library().gla_scan_bwd_workspace(B, H, T, D, 0), dev)
+    _enqueue("gla_scan_bwd", dev, gp, xp, hp, hcp, dop, dhp, dg.data_ptr(), dx.data_ptr(),
+             None if dh0 is None else dh0.data_ptr(), B, H, T, D, int(complement), dt,
+             None if ws is None else ws.data_ptr(), nb)
+    return dg, dx, dh0
+
+
+def scan_step(g, x, S, complement: bool = False):
+    """One token of scan_fwd: g, x [B,H,D]; S [B,H,D] fp32 updated in place.  Returns o [B,H,D]."""
+    dt, dev = _first(g, 3)
+    B, H, D = g.shape
+    gp, xp = _operand("g", g, g.dtype, g.shape, dev), _operand("x", x, g.dtype, g.shape, dev)
+    if S is None:
+        raise GLAError("scan_step needs the state S")
+    Sp = _operand("S", S, torch.float32, g.shape, dev)
+    o = torch.empty_like(g)
+    _enqueue("gla_scan_step", dev, gp, xp, Sp, o.data_ptr(), B, H, D, int(complement), dt)
+    return o
+
+
+_LAYOUTS = {"bhtd": 0, "bthd": 1}
+_NORM_KINDS = {"group": 0, "rms": 1}
+_ACTS = {"none": 0, "silu": 1, "sigmoid": 2}
+
+
+def _choice(name, value, table):
+    if value not in table:
+        raise GLAError(f"{name} must be one of {', '.join(table)}; got {value!r}")
+    return table[value]
+
+
+def _norm_args(x, z, w, b, layout):
+    dt, dev = _first(x, 4)
+    head_major = _choice("layout", layout, _LAYOUTS) == 0
+    B, H, T, D = x.shape if head_major else (x.shape[0], x.shape[2], x.shape[1], x.shape[3])
+    out = (B, T, H, D)
+    rows = H
+    for p in (w, b):
+        if p is not None:
+            rows = p.shape[0] if p.dim() == 2 else -1
+    if rows not in (1, H):
+        raise GLAError(f"w and b must be [H, D] or [1, D] with H = {H}")
+    xp, zp = _operand("x", x, x.dtype, x.shape, dev), _operand("z", z, x.dtype, out, dev)
+    wp, bp = (_operand(n, p, torch.float32, (rows, D), dev) for n, p in (("w", w), ("b", b)))
+    return dt, dev, out, rows, xp, zp, wp, bp
+
+
+def group_norm_fwd(x, z=None, w=None, b=None, kind: str = "group", act: str = "silu", eps: float = 1e-5,
+                   layout: str = "bhtd"):
+    """Norm of every head of a token, scaled and gated: y = (norm(x) * w + b) * act(z), or act(norm(x) * w + b)
+    without z.
+
+    x [B,H,T,D] (layout "bhtd", what the recurrences return) or [B,T,H,D] ("bthd"); z and the result are
+    [B,T,H,D], that is, channels last.  w, b: fp32 [H,D], or [1,D] shared by the heads.  kind: "group" (mean and
+    variance) or "rms"; act: "none", "silu", "sigmoid".
+    """
+    dt, dev, out, rows, xp, zp, wp, bp = _norm_args(x, z, w, b, layout)
+    B, T, H, D = out
+    y = torch.empty(out, dtype=x.dtype, device=dev)
+    _enqueue("gla_group_norm_fwd", dev, xp, zp, wp, bp, y.data_ptr(), B, H, T, D, rows,
+             _choice("kind", kind, _NORM_KINDS), _choice("act", act, _ACTS), eps, _LAYOUTS[layout], dt)
+    return y
+
+
+def group_norm_bwd(x, dy, z=None, w=None, b=None, kind: str = "group", act: str = "silu", eps: float = 1e-5,
+                   layout: str = "bhtd"):
+    """Backward of group_norm_fwd: returns (dx in x's layout, dz or None, dw or None, db or None)."""
+    dt, dev, out, rows, xp, zp, wp, bp = _norm_args(x, z, w, b, layout)
+    B, T, H, D = out
+    kind, act = _choice("kind", kind, _NORM_KINDS), _choice("act", act, _ACTS)
+    dyp = _operand("dy", dy, x.dtype, out, dev)
+    dx = torch.empty_like(x)
+    dz = None if z is None else torch.empty_like(z)
+    dw, db = (None if p is None else torch.empty_like(p) for p in (w, b))
+    ws, nb = _workspace(load_library().gla_group_norm_bwd_workspace(B, H, T, D, rows, w is not None, b is not None), dev)
+    _enqueue("gla_group_norm_bwd", dev, xp, zp, wp, bp, dyp, dx.data_ptr(),
+             *(None if t is None else t.data_ptr() for t in (dz, dw, db)), B, H, T, D, rows, kind, act, eps,
+             _LAYOUTS[layout], dt, None if ws is None else ws.data_ptr(), nb)
+    return dx, dz, dw, db
+
+
+def rotary_frequencies(R: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                       trained: int = 0, slow: float = 1.0, fast: float = 32.0, device="cuda"):
+    """Frequencies for rotary (radians a position, float64 [R/2]) and the scale of the rotated channels.
+
+    freq_i = base^(-2i/R), changed for positions beyond the `trained` length by `factor`:
+      "none"    as it is
+      "linear"  freq / factor: positions are interpolated
+      "ntk"     base * factor^(R/(R-2)): the slowest pair is interpolated, the fastest left alone
+      "yarn"    pairs that turn more than `fast` times over the trained length are left alone, those that turn
+                less than `slow` times are interpolated, a ramp in between; scale = 0.1 ln(factor) + 1
+    Returns (freq, scale).  Made once for a model; the calls take them as they are.
+    """
+    if R < 2 or R % 2 or not base > 1 or not factor >= 1:
+        raise GLAError(f"rotary_frequencies: needs an even R >= 2, base > 1 and factor >= 1; got {R}, {base}, {factor}")
+    i = torch.arange(0, R, 2, dtype=torch.float64)
+    scale = 1.0
+    if scaling == "ntk":
+        if R <= 2:
+            raise GLAError("rotary_frequencies: ntk scaling needs R > 2")
+        base = base * factor ** (R / (R - 2))
+    freq = base ** (-i / R)
+    if scaling == "linear":
+        freq = freq / factor
+    elif scaling == "yarn":
+        if trained <= 0 or not 0 < slow < fast:
+            raise GLAError("rotary_frequencies: yarn scaling needs the trained length and 0 < slow < fast")
+
+        def pair(turns):  # the (fractional) pair that turns so often over the trained length
+            return R * math.log(trained / (turns * 2 * math.pi)) / (2 * math.log(base))
+
+        lo, hi = max(0, math.floor(pair(fast))), min(R - 1, math.ceil(pair(slow)))
+        ramp = ((i / 2 - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        freq = freq * (1 - ramp) + freq / factor * ramp
+        scale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in ("none", "ntk"):
+        raise GLAError(f"scaling must be one of none, linear, ntk, yarn; got {scaling!r}")
+    return freq.to(device), scale
+
+
+def _rotary(q, k, freq, pos, pos0, interleaved, scale, inverse, in_layout, out_layout):
+    dt, dev = _first(q, 4)
+    lin, lout = _choice("layout", in_layout, _LAYOUTS), _choice("out_layout", out_layout, _LAYOUTS)
+    B, D = q.shape[0], q.shape[3]
+    T, Hq = (q.shape[2], q.shape[1]) if lin == 0 else (q.shape[1], q.shape[2])
+    Hk = 0
+    if k is not None:
+        if k.dim() != 4:
+            raise GLAError(f"k must have 4 dimensions, got shape {tuple(k.shape)}")
+        Hk = k.shape[1] if lin == 0 else k.shape[2]
+    shape = (lambda H, lay: (B, H, T, D) if lay == 0 else (B, T, H, D))
+    qp, kp = _operand("q", q, q.dtype, shape(Hq, lin), dev), _operand("k", k, q.dtype, shape(Hk, lin), dev)
+    if freq.dim() != 1:
+        raise GLAError(f"freq must be [R/2], got shape {tuple(freq.shape)}")
+    fp = _operand("freq", freq, torch.float64, freq.shape, dev)
+    rows = 0
+    if pos is not None:
+        rows = 1 if pos.dim() == 1 else B
+    pp = _operand("pos", pos, torch.int64, (T,) if rows == 1 and pos.dim() == 1 else (B, T), dev)
+    qo = torch.empty(shape(Hq, lout), dtype=q.dtype, device=dev)
+    ko = None if k is None else torch.empty(shape(Hk, lout), dtype=q.dtype, device=dev)
+    _enqueue("gla_rotary", dev, qp, kp, qo.data_ptr(), None if ko is None else ko.data_ptr(), fp, pp, int(pos0), rows,
+             B, Hq, Hk, T, D, 2 * freq.shape[0], float(scale), int(interleaved), int(inverse), lin, lout, dt)
+    return qo, ko
+
+
+def rotary(q, k, freq, pos=None, pos0: int = 0, interleaved: bool = False, scale: float = 1.0, layout: str = "bhtd",
+           out_layout: str = "bhtd"):
+    """Rotary positions of q and k (k may be None): returns (q', k') in out_layout.
+
+    q [B,Hq,T,D], k [B,Hk,T,D] (layout "bhtd") or [B,T,H,D] ("bthd").  freq: float64 [R/2], radians a position for
+    the pairs of the first R channels (rotary_frequencies).  Positions are pos0 + t, or pos0 + pos with pos int64
+    [T] or [B,T].  Pairs are (i, i + R/2), or (2i, 2i+1) when interleaved; channels from R on are copied.
+    """
+    return _rotary(q, k, freq, pos, pos0, interleaved, scale, False, layout, out_layout)
+
+
+def rotary_bwd(dq, dk, freq, pos=None, pos0: int = 0, interleaved: bool = False, scale: float = 1.0,
+               layout: str = "bhtd", out_layout: str = "bhtd"):
+    """Backward of rotary, called with the forward's arguments: dq, dk come in out_layout, the result in layout."""
+    return _rotary(dq, dk, freq, pos, pos0, interleaved, scale, True, out_layout, layout)

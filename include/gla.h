@@ -252,6 +252,95 @@ int gla_msgla_hold_bwd(const void* dout, void* dy, int B, int H, int T, int D, i
                        void* stream);
 
 /* ---------------------------------------------------------------------------------------
+ * gla_scan_* - the elementwise gated linear recurrence: a state of one value per channel instead
+ * of a matrix, scanned over the sequence.
+ *     h_t = a_t h_{t-1} + b_t ,   o_t = h_t ,   a_t = exp g_t
+ *     b_t = x_t                 (GLA_SCAN_ADD)
+ *     b_t = (1 - a_t) x_t       (GLA_SCAN_COMPLEMENT: the input gate is what the forget gate leaves;
+ *                                1 - a is formed without cancellation for g near 0)
+ * The gate is the log of the decay as for gla_chunk_fwd ("MS-GLA", section 2.1: a data-dependent
+ * forget gate), g <= 0; here g = -inf is allowed too and restarts the channel at that token (packed
+ * sequences), provided the state before it is finite.
+ *   gla_scan_fwd   in : g, x [B,H,T,D]; h0 [B,H,D] fp32 (optional)
+ *                  out: o [B,H,T,D]; hT [B,H,D] fp32 (optional);
+ *                       hc [B,H,ceil(T/64),D] fp32 (optional): the state before tokens 0, 64, 128, ...
+ *   gla_scan_bwd   in : g, x, h0 as above; hc as gla_scan_fwd wrote it (optional: when it is NULL the
+ *                       states are recomputed from g, x and h0 into the workspace, else h0 is not read);
+ *                       dO [B,H,T,D]; dhT [B,H,D] fp32 (optional)
+ *                  out: dg, dx [B,H,T,D]; dh0 [B,H,D] fp32 (optional)
+ *                  with d_t = dO_t + a_{t+1} d_{t+1} (the last token's also takes dhT):
+ *                  dx = d, dg = a h_{t-1} d  or, for the complement, dx = (1 - a) d,
+ *                  dg = a (h_{t-1} - x) d;  dh0 = a_1 d_1.
+ *   gla_scan_step  one token: g, x [B,H,D], S [B,H,D] fp32 (read, then overwritten), o [B,H,D].
+ * A model without heads passes its [B,T,C] tensors as H = 1, D = C.  D >= 1 and B*H*ceil(D/16) <=
+ * 2^27 (else GLA_ERR_UNSUPPORTED); T == 0 as for gla_chunk_fwd.  Pointers of these and the following
+ * operators need the alignment of their element type only; 16-byte aligned ones with rows of a
+ * multiple of 16 bytes run the vector form.  Results do not depend on the number of SMs or on the
+ * order in which blocks run.
+ * ------------------------------------------------------------------------------------- */
+typedef enum { GLA_SCAN_ADD = 0, GLA_SCAN_COMPLEMENT = 1 } gla_scan_input;
+
+int gla_scan_fwd(const void* g, const void* x, const float* h0, void* o, float* hT, float* hc, int B, int H,
+                 int T, int D, int input, int dtype, void* stream);
+size_t gla_scan_bwd_workspace(int B, int H, int T, int D, int have_hc);
+int gla_scan_bwd(const void* g, const void* x, const float* h0, const float* hc, const void* dO,
+                 const float* dhT, void* dg, void* dx, float* dh0, int B, int H, int T, int D, int input,
+                 int dtype, void* workspace, size_t workspace_bytes, void* stream);
+int gla_scan_step(const void* g, const void* x, float* S, void* o, int B, int H, int D, int input, int dtype,
+                  void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * gla_group_norm_* - the norm and output gate behind a recurrence: every head's D outputs of a
+ * token are one group, normalised on their own, scaled, gated, and left channels last for the output
+ * projection (statistics over the tokens would let a causal model see the future).
+ *     n = (x - mean) / sqrt(var + eps)          GLA_NORM_GROUP (var is the biased variance)
+ *     n = x / sqrt(mean(x^2) + eps)             GLA_NORM_RMS
+ *     u = n * w + b ;   y = u * act(z)  or, without z,  y = act(u)
+ *   act: GLA_ACT_NONE (identity), GLA_ACT_SILU, GLA_ACT_SIGMOID
+ *   gla_group_norm_fwd  in : x in `layout` (GLA_LAYOUT_BHTD [B,H,T,D], what the operators above write,
+ *                            or GLA_LAYOUT_BTHD [B,T,H,D]); z [B,T,H,D] (optional);
+ *                            w, b [weight_rows, D] fp32 (optional: ones, zeros)
+ *                       out: y [B,T,H,D]
+ *   gla_group_norm_bwd  in : x, z, w, b, dy [B,T,H,D]
+ *                       out: dx in `layout`; dz [B,T,H,D] (optional; needs z);
+ *                            dw, db [weight_rows, D] fp32 (optional), summed in a fixed order
+ * weight_rows: H (a weight for each channel) or 1 (one row shared by the heads).  1 <= D <= 8192
+ * (else GLA_ERR_UNSUPPORTED); eps > 0 and finite.  T == 0: dw and db are zeroed, nothing else is
+ * written.  Statistics and sums are fp32.  Workspace of the backward: per-block partial sums of dw
+ * and db (0 bytes when neither is asked for).
+ * ------------------------------------------------------------------------------------- */
+typedef enum { GLA_NORM_GROUP = 0, GLA_NORM_RMS = 1 } gla_norm_kind;
+typedef enum { GLA_ACT_NONE = 0, GLA_ACT_SILU = 1, GLA_ACT_SIGMOID = 2 } gla_activation;
+typedef enum { GLA_LAYOUT_BHTD = 0, GLA_LAYOUT_BTHD = 1 } gla_layout;
+
+int gla_group_norm_fwd(const void* x, const void* z, const float* w, const float* b, void* y, int B, int H,
+                       int T, int D, int weight_rows, int kind, int act, float eps, int layout, int dtype,
+                       void* stream);
+size_t gla_group_norm_bwd_workspace(int B, int H, int T, int D, int weight_rows, int need_dw, int need_db);
+int gla_group_norm_bwd(const void* x, const void* z, const float* w, const float* b, const void* dy, void* dx,
+                       void* dz, float* dw, float* db, int B, int H, int T, int D, int weight_rows, int kind,
+                       int act, float eps, int layout, int dtype, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * gla_rotary - rotary positions of q and, in the same launch, k.
+ *     (u_i, v_i) <- scale * (u_i cos A_i - v_i sin A_i,  v_i cos A_i + u_i sin A_i),  A_i = p * freq_i
+ * for the R/2 pairs of the first R channels of every head: (u_i, v_i) are channels (i, i + R/2), or
+ * (2i, 2i + 1) when `interleaved`.  Channels R .. D-1 are copied as they are.
+ *   in : q [B,Hq,T,D], k [B,Hk,T,D] (NULL with Hk = 0) in `in_layout`; freq [R/2] float64, radians a
+ *        position; pos int64: NULL with pos_rows = 0 (p = pos0 + t), [T] with pos_rows = 1 or [B,T]
+ *        with pos_rows = B (p = pos0 + pos)
+ *   out: qo, ko in `out_layout`; with equal layouts qo = q and ko = k (in place) are allowed
+ * The angle is formed and reduced to a turn in 64 bits, so far positions (|p * freq| < 2^51) keep
+ * fp32 accuracy; the rotation is fp32 and rounded once.  inverse != 0 rotates by -A with the same
+ * scale, which is the transpose: the backward of a call is the call with inverse set and the layouts
+ * exchanged.  1 <= D <= 8192, R even, 2 <= R <= D; scale finite.  T == 0 enqueues nothing.
+ * ------------------------------------------------------------------------------------- */
+int gla_rotary(const void* q, const void* k, void* qo, void* ko, const double* freq, const long long* pos,
+               long long pos0, int pos_rows, int B, int Hq, int Hk, int T, int D, int R, float scale,
+               int interleaved, int inverse, int in_layout, int out_layout, int dtype, void* stream);
+
+/* ---------------------------------------------------------------------------------------
  * gla_device_error - read (and optionally clear) the device-side error latch.
  * Synchronises `stream`, then stores GLA_OK or the first error a kernel recorded since the
  * last reset (GLA_ERR_TIMEOUT: a bounded wait ran out) in *code.  Returns GLA_ERR_CUDA if
