@@ -4,20 +4,21 @@
 //
 // HBM-bound: g and x are read once and o written once.  A run of tokens acts on the state in front of it as
 // h -> A h + H with A the product of its a's and H its end state from zero, and two runs one after the other
-// act as (A2 A1, A2 H1 + H2).  So every thread reduces a run of R tokens of VEC neighbouring channels to (A, H),
-// the pairs are joined in token order across the lanes of a warp (shuffles), the warps of a block (shared
-// memory) and the blocks of a cluster (their shared memory), and then each thread walks its run again from the
-// state that enters it.
+// act as (A2 A1, A2 H1 + H2).  So every thread reduces a run of R tokens of two neighbouring channels to (A, H), the
+// pairs are joined in token order across the lanes of a warp (shuffles), the warps of a block (shared memory) and the
+// blocks of a cluster (their shared memory), and then each thread walks its run again from the state that enters it.
 //
-// Split: a block owns a slab of LPR * VEC channels and steps through the tokens; a step is a tile of
-// 8 (32 / LPR) R tokens.  Where there are too few slabs to fill the SMs, K blocks of a cluster share a slab and take
-// its tiles in turn.  Each step every block sends its (A, H) to all blocks of the cluster (st.async onto an
-// mbarrier in the receiver's shared memory); every block folds all K of them, in token order, into a carry of its
-// own.  So nothing goes through global memory, nothing waits outside the cluster, whose blocks run together, and the
-// order of all operations is fixed by the sizes.
+// Split: a block owns a slab of 2 LPR channels and steps through the tokens; a step is a tile of 8 (32 / LPR) R
+// tokens.  Where there are too few slabs to fill the SMs, K blocks of a cluster share a slab and take its tiles in
+// turn.  Each step every block sends its (A, H) to all blocks of the cluster (st.async onto an mbarrier in the
+// receiver's shared memory); every block folds all K of them, in token order, into a carry of its own.  So nothing
+// goes through global memory, nothing waits outside the cluster, whose blocks run together, and the order of all
+// operations is fixed by the sizes.
 //
-// The tiles are copied asynchronously, two steps ahead, into places of shared memory that only the copying
-// thread reads, so they need no barrier; a step takes one __syncthreads.
+// What a step costs is instructions (a value has 6 bytes to move at bf16, about 30 issue slots an SM at full
+// bandwidth): two channels a thread go through the packed fp32 pair arithmetic of sm_100a, tiles come by TMA, and a
+// step has one __syncthreads, which also says that the tile's values are in registers and its place can be filled
+// again.
 //
 // The backward walks the tiles in reverse with e_t = a_t d_t as the state: d_t = dO_t + e_{t+1}, so a run acts as
 // e -> A e + E with the same A.  The states h_{t-1} that dg needs are recomputed in fp32 inside the tile, from
@@ -30,6 +31,7 @@
 
 #include "../../include/gla.h"
 #include "fast_path.cuh"
+#include "fused_common.cuh"
 #include "scan_cluster.cuh"
 #include "vec.cuh"
 
@@ -37,440 +39,477 @@ namespace {
 
 using gla::bf16;
 using gla::ldf;
-using gla::Pack;
 using gla::stf;
 namespace cl = gla::cluster;
+namespace sm = gla::sm100;
 
-constexpr int kKeep = 64;   // tokens between the kept states
-constexpr int kWarps = 8;   // warps a block
-constexpr int kMaxK = 8;    // blocks a cluster
-constexpr int kStages = 2;  // tiles in flight or in use
+constexpr int kKeep = 64;          // tokens between the kept states
+constexpr int kWarps = 8;          // warps a block
+constexpr int kNT = kWarps * 32;   // threads a block
 
-// a = exp g and 1 - a.  Near g = 0 both come from exp g - 1 = g (1 + g/2 (1 + g/3 (...))), so that neither the
-// 1 - a of a slow gate nor a long product of a's loses its leading digits; the series ends five terms in, where
-// |g| < 1/8 leaves a relative error below g^5/720 < 2^-24.  Elsewhere a state forgets within a few dozen tokens,
-// and the exponential's own error (2^-22 for the approximate one at bf16) has no time to add up.
+// ---- two fp32 values in a register pair -------------------------------------------------------------
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float x) { return f2(x, x); }
+__device__ __forceinline__ float lo(F2 a) {
+  float x, y;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v));
+  return x;
+}
+__device__ __forceinline__ float hi(F2 a) {
+  float x, y;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v));
+  return y;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 shfl2(F2 a, int src) {
+  return f2(__shfl_sync(0xffffffffu, lo(a), src), __shfl_sync(0xffffffffu, hi(a), src));
+}
+
+// Two neighbouring values as they lie in memory.
 template <typename T>
-__device__ __forceinline__ float decay(float g, float* rest) {
-  float p = fmaf(g, 1.f / 120.f, 1.f / 24.f);
-  p = fmaf(g, p, 1.f / 6.f);
-  p = fmaf(g, p, 0.5f);
-  p = fmaf(g, p, 1.f) * g;
-  const float e = sizeof(T) == 2 ? __expf(g) : expf(g);
-  const bool slow = fabsf(g) < 0.125f;
-  *rest = slow ? -p : 1.f - e;
-  return slow ? 1.f + p : e;
-}
-
-struct Args {
-  const void *g, *x, *dO;
-  const float *first;  // h0 (forward), dhT (backward), or null
-  const float* hc_in;  // backward: kept states
-  void *o, *dg, *dx;
-  float *last, *hc;    // hT (forward), dh0 (backward); kept states (forward); or null
-  int T, D, slabs;     // slabs of channels a head
-  int steps, tiles, K;
-  unsigned int* latch;
-};
-
-// A thread's place: VEC channels from `c` of the block's slab, run `run` of the tile.
-template <int VEC, int LPR>
-struct Place {
-  int lane_c, run_in_warp, warp, c;
-  size_t bh;
-  uint32_t rank;
-  __device__ __forceinline__ Place(const Args& a, bool clustered) {
-    const int lane = threadIdx.x & 31;
-    lane_c = lane % LPR, run_in_warp = lane / LPR, warp = threadIdx.x >> 5;
-    const uint32_t col = clustered ? blockIdx.x / (uint32_t)a.K : blockIdx.x;
-    rank = clustered ? cl::block_rank() : 0;
-    bh = col / (uint32_t)a.slabs;
-    c = ((int)(col - (uint32_t)bh * (uint32_t)a.slabs) * LPR + lane_c) * VEC;
+struct Two;
+template <>
+struct Two<bf16> {
+  typedef uint32_t Raw;
+  static __device__ __forceinline__ F2 wide(Raw w) {
+    return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
   }
+  static __device__ __forceinline__ Raw narrow(F2 v) { return gla::fast::pack2(lo(v), hi(v)); }
+};
+template <>
+struct Two<float> {
+  typedef uint64_t Raw;
+  static __device__ __forceinline__ F2 wide(Raw w) { return F2{w}; }
+  static __device__ __forceinline__ Raw narrow(F2 v) { return v.v; }
 };
 
-// Copy this thread's VEC channels of a token into its own place: asynchronously where the piece has 4 bytes or more.
-template <typename T, int VEC>
-__device__ __forceinline__ void fetch(char* place, const T* src, bool in) {
-  constexpr int BYTES = VEC * (int)sizeof(T);
-  if constexpr (BYTES >= 4) {
-    cl::copy_async<BYTES>(gla::sm100::smem_u32(place), src, in);
+// a = exp g and, with REST, 1 - a.  Near g = 0 both come from exp g - 1 = g (1 + g/2 (1 + g/3 (...))), so that
+// neither the 1 - a of a slow gate nor a long product of a's loses its leading digits; the series ends five terms
+// in, where |g| < 1/8 leaves a relative error below g^5/720 < 2^-24.  Elsewhere a state forgets within a few dozen
+// tokens, and the exponential's own error (2^-22 for the approximate one at bf16) has no time to add up.
+template <typename T, bool REST>
+__device__ __forceinline__ F2 decay(F2 g, F2* rest) {
+  F2 t = fma2(g, f2(1.f / 120.f), f2(1.f / 24.f));
+  t = fma2(g, t, f2(1.f / 6.f));
+  t = fma2(g, t, f2(0.5f));
+  t = fma2(g, t, f2(1.f));
+  const F2 near = fma2(t, g, f2(1.f));
+  F2 far;
+  if constexpr (sizeof(T) == 2) {
+    const F2 y = mul2(g, f2(gla::fast::kLog2e));
+    far = f2(gla::fast::ex2(lo(y)), gla::fast::ex2(hi(y)));
   } else {
-    T v;
-    stf(&v, 0.f);
-    if (in) v = *src;
-    *reinterpret_cast<T*>(place) = v;
+    far = f2(expf(lo(g)), expf(hi(g)));
   }
+  const bool s0 = fabsf(lo(g)) < 0.125f, s1 = fabsf(hi(g)) < 0.125f;
+  if constexpr (REST) {
+    const F2 rn = mul2(t, mul2(g, f2(-1.f))), rf = fma2(far, f2(-1.f), f2(1.f));
+    *rest = f2(s0 ? lo(rn) : lo(rf), s1 ? hi(rn) : hi(rf));
+  }
+  return f2(s0 ? lo(near) : lo(far), s1 ? hi(near) : hi(far));
 }
 
-// The pair (A, H) of VEC channels, and what follows it.
-template <int VEC>
+// The action h -> A h + H of a run on two channels.
 struct Pair {
-  float A[VEC], H[VEC];
-  __device__ __forceinline__ void identity() {
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) A[j] = 1.f, H[j] = 0.f;
-  }
+  F2 A, H;
+  __device__ __forceinline__ void identity() { A = f2(1.f), H = f2(0.f); }
   // this := n after this
   __device__ __forceinline__ void then(const Pair& n) {
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      H[j] = fmaf(n.A[j], H[j], n.H[j]);
-      A[j] *= n.A[j];
-    }
+    H = fma2(n.A, H, n.H);
+    A = mul2(A, n.A);
   }
+  __device__ __forceinline__ F2 of(F2 h) const { return fma2(A, h, H); }
 };
 
 // Exclusive join over the runs of a warp, in token order (or against it): `p` becomes what lies before this
 // lane's run, `all` the whole warp's.
-template <int VEC, int LPR, bool REVERSE>
-__device__ __forceinline__ void join_warp(Pair<VEC>& p, Pair<VEC>& all, int run) {
+template <int LPR, bool REVERSE>
+__device__ __forceinline__ void join_warp(Pair& p, Pair& all, int run) {
   constexpr int RUNS = 32 / LPR;
   if constexpr (RUNS == 1) {
     all = p;
     p.identity();
   } else {
-    const int at = REVERSE ? RUNS - 1 - run : run;
+    const int lane = threadIdx.x & 31, at = REVERSE ? RUNS - 1 - run : run;
+    auto from = [&](int d) { return (lane + (REVERSE ? d : -d) * LPR) & 31; };
 #pragma unroll
     for (int d = 1; d < RUNS; d *= 2) {
-      Pair<VEC> q;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        q.A[j] = REVERSE ? __shfl_down_sync(0xffffffffu, p.A[j], d * LPR) : __shfl_up_sync(0xffffffffu, p.A[j], d * LPR);
-        q.H[j] = REVERSE ? __shfl_down_sync(0xffffffffu, p.H[j], d * LPR) : __shfl_up_sync(0xffffffffu, p.H[j], d * LPR);
-      }
+      Pair q;
+      q.A = shfl2(p.A, from(d)), q.H = shfl2(p.H, from(d));
       if (at >= d) {
         q.then(p);
         p = q;
       }
     }
-    const int src = (threadIdx.x & 31) % LPR + (REVERSE ? 0 : (RUNS - 1) * LPR);
-    Pair<VEC> q;
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      all.A[j] = __shfl_sync(0xffffffffu, p.A[j], src);
-      all.H[j] = __shfl_sync(0xffffffffu, p.H[j], src);
-      q.A[j] = REVERSE ? __shfl_down_sync(0xffffffffu, p.A[j], LPR) : __shfl_up_sync(0xffffffffu, p.A[j], LPR);
-      q.H[j] = REVERSE ? __shfl_down_sync(0xffffffffu, p.H[j], LPR) : __shfl_up_sync(0xffffffffu, p.H[j], LPR);
-    }
+    const int last = lane % LPR + (REVERSE ? 0 : (RUNS - 1) * LPR);
+    Pair q;
+    q.A = shfl2(p.A, from(1)), q.H = shfl2(p.H, from(1));
+    all.A = shfl2(p.A, last), all.H = shfl2(p.H, last);
     if (at == 0) p.identity();
     else p = q;
   }
 }
 
-// Shared memory of the cluster's exchange: two slots, each with every rank's pair.
-template <int VEC, int LPR>
+// How a block's tiles come into shared memory (rows of 2 LPR values, one a token):
+//   kTma       one copy of the whole tile by TMA; rows and tensors start on 16 bytes
+//   kByThread  every thread copies what it will read itself, two values or one at a time, asynchronously where
+//              they have 4 bytes at least
+enum Load { kTma = 0, kByThread = 1 };
+
+struct Args {
+  const void* in[3];   // g, x and, in the backward, dO
+  const float* first;  // h0 (forward), dhT (backward), or null
+  const float* hc_in;  // backward: kept states
+  void *out0, *out1;   // o (may be null), or dx and dg
+  float *last, *hc;    // hT (forward), dh0 (backward); kept states (forward); or null
+  int T, D, slabs;     // slabs of channels a head
+  int steps, tiles, K;
+  int pairs;           // kByThread: two values at a time are aligned
+  unsigned int* latch;
+};
+struct Maps {
+  CUtensorMap m[3];
+};
+
+// Cluster exchange: two slots with every rank's pair, each on an mbarrier.
+template <int LPR, int MAXK>
 struct Exchange {
-  float slot[2][kMaxK][LPR][2 * VEC];
+  float4 slot[2][MAXK][LPR];
   uint64_t bar[2];
 };
 
-// Sends the block's pair to the cluster, waits for all pairs, moves `carry` over all of them and leaves in
-// `enter` the state that enters this block's tile.  A slot is used again two steps later: a block sends for step
-// s + 2 after it has taken everybody's pair of step s + 1, and a block sends that only after the __syncthreads
-// behind its reads of step s.
-template <int VEC, int LPR>
-__device__ __forceinline__ void exchange(Exchange<VEC, LPR>& ex, const Pair<VEC>& block, float (&carry)[VEC],
-                                         float (&enter)[VEC], int step, int K, uint32_t rank, int warp, int run,
-                                         int lane_c, bool& alive, unsigned int* latch) {
-  const int s = step & 1;
-  if (warp < K && run == 0) {
-    float v[2 * VEC];
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) v[j] = block.A[j], v[VEC + j] = block.H[j];
-    cl::store_async(cl::peer(gla::sm100::smem_u32(&ex.slot[s][rank][lane_c][0]), warp), v,
-                    cl::peer(gla::sm100::smem_u32(&ex.bar[s]), warp));
-  }
-  if (alive) {
-    alive = cl::wait(gla::sm100::smem_u32(&ex.bar[s]), (step >> 1) & 1, latch);
-    // the slot's next use, two steps on
-    if (alive && threadIdx.x == 0)
-      gla::sm100::mbar_arrive_expect_tx(&ex.bar[s], (uint32_t)(K * LPR * 2 * VEC * sizeof(float)));
-  }
-  for (int r = 0; r < K; ++r) {
-    if (r == (int)rank)
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) enter[j] = carry[j];
-    const float* v = ex.slot[s][r][lane_c];
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) carry[j] = fmaf(v[j], carry[j], v[VEC + j]);
-  }
-}
+template <typename T, int LPR, int R, int NIN, int STAGES, int MAXK, bool CLUSTER, int LOAD>
+struct Block {
+  static constexpr int RUNS = 32 / LPR, TILE = kWarps * RUNS * R, CW = 2 * LPR;
+  static constexpr int ROW = CW * (int)sizeof(T), ARRAY = TILE * ROW, STAGE = NIN * ARRAY;
+  typedef typename Two<T>::Raw Raw;
+  typedef Exchange<CLUSTER ? LPR : 1, CLUSTER ? MAXK : 1> Ex;
 
-template <int VEC, int LPR>
-__device__ __forceinline__ void open_exchange(Exchange<VEC, LPR>& ex, int K) {
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < 2; ++s) gla::sm100::mbar_init(&ex.bar[s], 1);
-    gla::sm100::fence_mbar_init();
-    for (int s = 0; s < 2; ++s)
-      gla::sm100::mbar_arrive_expect_tx(&ex.bar[s], (uint32_t)(K * LPR * 2 * VEC * sizeof(float)));
-  }
-  cl::sync();
-}
+  const Args& a;
+  char* stage;
+  uint64_t* full;  // [STAGES]
+  Ex& ex;
+  int lane_c, run, warp, c, slab;
+  size_t bh;
+  uint32_t rank;
+  bool alive, mine0, mine1;
 
-template <typename T, int VEC, int LPR, int R, bool COMP, bool CLUSTER>
-__global__ void __launch_bounds__(kWarps * 32, 2) scan_fwd_kernel(const Args a) {
-  constexpr int NT = kWarps * 32, RUNS = 32 / LPR, TILE = kWarps * RUNS * R, PIECE = VEC * (int)sizeof(T);
-  extern __shared__ __align__(16) char stage[];  // [kStages][2][R][NT] pieces
-  __shared__ __align__(16) float tot[2][kWarps][LPR][2 * VEC];
-  __shared__ __align__(16) Exchange<VEC, CLUSTER ? LPR : 1> ex;
-  const Place<VEC, LPR> at(a, CLUSTER);
-  if constexpr (CLUSTER) open_exchange(ex, a.K);
-  const T *g = (const T*)a.g, *x = (const T*)a.x;
-  const bool mine = at.c < a.D;
-  const size_t base = at.bh * (size_t)a.T * a.D + (mine ? at.c : 0);
-  float carry[VEC];
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) carry[j] = mine && a.first ? a.first[at.bh * a.D + at.c + j] : 0.f;
-  bool alive = true;
-
-  auto first_token = [&](int step) {
-    return ((long long)step * a.K + at.rank) * TILE + (at.warp * RUNS + at.run_in_warp) * R;
-  };
-  auto place = [&](int step, int which, int i) {
-    return stage + ((((step % kStages) * 2 + which) * R + i) * NT + threadIdx.x) * PIECE;
-  };
-  auto prefetch = [&](int step) {
-    if (step < a.steps) {
-      const long long t0 = first_token(step);
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const bool in = mine && t0 + i < a.T;
-        const size_t p = in ? base + (size_t)(t0 + i) * a.D : 0;
-        fetch<T, VEC>(place(step, 0, i), g + p, in);
-        fetch<T, VEC>(place(step, 1, i), x + p, in);
-      }
+  __device__ __forceinline__ Block(const Args& args, char* smem, uint64_t* bars, Ex& e)
+      : a(args), stage(smem), full(bars), ex(e), alive(true) {
+    const int lane = threadIdx.x & 31;
+    lane_c = lane % LPR, run = lane / LPR, warp = threadIdx.x >> 5;
+    const uint32_t col = CLUSTER ? blockIdx.x / (uint32_t)a.K : blockIdx.x;
+    rank = CLUSTER ? cl::block_rank() : 0;
+    bh = col / (uint32_t)a.slabs;
+    slab = (int)(col - (uint32_t)bh * (uint32_t)a.slabs);
+    c = slab * CW + lane_c * 2;
+    mine0 = c < a.D, mine1 = c + 1 < a.D;
+    if (threadIdx.x == 0) {
+      if constexpr (LOAD == kTma)
+        for (int s = 0; s < STAGES; ++s) sm::mbar_init(&full[s], 1);
+      if constexpr (CLUSTER)
+        for (int s = 0; s < 2; ++s) sm::mbar_init(&ex.bar[s], 1);
+      sm::fence_mbar_init();
+      if constexpr (CLUSTER)
+        for (int s = 0; s < 2; ++s) sm::mbar_arrive_expect_tx(&ex.bar[s], (uint32_t)(a.K * LPR * 16));
     }
-    cl::copy_commit();
-  };
-  for (int s = 0; s < kStages; ++s) prefetch(s);
+    if constexpr (CLUSTER) cl::sync();
+    else __syncthreads();
+  }
+
+  __device__ __forceinline__ size_t row(long long t) const { return (bh * (size_t)a.T + (size_t)t) * a.D + c; }
+  __device__ __forceinline__ int first_row() const { return (warp * RUNS + run) * R; }
+
+  // Values of a state row [bh][D].
+  __device__ __forceinline__ F2 state(const float* p) const {
+    return f2(p && mine0 ? p[bh * a.D + c] : 0.f, p && mine1 ? p[bh * a.D + c + 1] : 0.f);
+  }
+  __device__ __forceinline__ void keep(float* p, F2 v) const {
+    if (mine0) p[0] = lo(v);
+    if (mine1) p[1] = hi(v);
+  }
+
+  // Starts the copy of the tile whose first token is `tile` (a tile outside the sequence reads as zeros) for
+  // step `step`; with kTma by one thread, when all threads have taken the values that lay there.
+  __device__ __forceinline__ void prefetch(const Maps& maps, int step, long long tile) {
+    char* at = stage + (step % STAGES) * STAGE;
+    if constexpr (LOAD == kTma) {
+      if (step < a.steps && alive && threadIdx.x == 0) {
+        uint64_t* bar = &full[step % STAGES];
+        sm::mbar_arrive_expect_tx(bar, STAGE);
+        const int t = tile < 0 || tile > a.T ? a.T : (int)tile;
+        for (int n = 0; n < NIN; ++n) sm::tma_load_3d(at + n * ARRAY, &maps.m[n], bar, slab * CW, t, (int)bh);
+      }
+    } else {
+      if (step < a.steps) {
+        const long long t0 = tile + first_row();
+        char* p = at + first_row() * ROW + lane_c * 2 * sizeof(T);
+#pragma unroll
+        for (int n = 0; n < NIN; ++n)
+#pragma unroll
+          for (int i = 0; i < R; ++i, p += ROW) {
+            if (i == 0) p = at + n * ARRAY + first_row() * ROW + lane_c * 2 * sizeof(T);
+            const bool in = tile >= 0 && t0 + i < a.T;
+            const T* src = (const T*)a.in[n] + (in && mine0 ? row(t0 + i) : 0);
+            if (a.pairs) {
+              cl::copy_async<2 * (int)sizeof(T)>(sm::smem_u32(p), src, in && mine0);
+            } else if constexpr (sizeof(T) == 4) {
+              cl::copy_async<4>(sm::smem_u32(p), src, in && mine0);
+              cl::copy_async<4>(sm::smem_u32(p + 4), in && mine1 ? src + 1 : src, in && mine1);
+            } else {
+              T v0, v1;
+              stf(&v0, 0.f), stf(&v1, 0.f);
+              if (in && mine0) v0 = src[0];
+              if (in && mine1) v1 = src[1];
+              reinterpret_cast<T*>(p)[0] = v0;
+              reinterpret_cast<T*>(p)[1] = v1;
+            }
+          }
+      }
+      cl::copy_commit();
+    }
+  }
+  __device__ __forceinline__ void arrived(int step) {
+    if constexpr (LOAD == kTma) {
+      if (alive) alive = sm::mbar_wait(&full[step % STAGES], (step / STAGES) & 1, a.latch);
+    } else {
+      cl::copy_wait<STAGES - 1>();
+    }
+  }
+  __device__ __forceinline__ Raw value(int step, int which, int i) const {
+    return *reinterpret_cast<const Raw*>(stage + (step % STAGES) * STAGE + which * ARRAY + (first_row() + i) * ROW +
+                                         lane_c * 2 * sizeof(T));
+  }
+  __device__ __forceinline__ void store(void* out, size_t at, F2 v) const {
+    T* p = (T*)out + at;
+    if (LOAD == kTma || a.pairs) {
+      *reinterpret_cast<Raw*>(p) = Two<T>::narrow(v);
+    } else {
+      stf(p, lo(v));
+      if (mine1) stf(p + 1, hi(v));
+    }
+  }
+
+  // Sends the block's pair to the cluster, waits for all pairs, moves `carry` over all of them and returns the
+  // state that enters this block's tile.  A slot is used again two steps later: a block sends for step s + 2 after
+  // it has taken everybody's pair of step s + 1, and a block sends that only after the __syncthreads behind its
+  // reads of step s.
+  __device__ __forceinline__ F2 exchange(const Pair& block, F2& carry, int step) {
+    F2 enter = carry;
+    if constexpr (CLUSTER) {
+      const int s = step & 1;
+      if (run == 0) {
+        const float v[4] = {lo(block.A), hi(block.A), lo(block.H), hi(block.H)};
+        for (int r = warp; r < a.K; r += kWarps)
+          cl::store_async(cl::peer(sm::smem_u32(&ex.slot[s][rank][lane_c]), r), v, cl::peer(sm::smem_u32(&ex.bar[s]), r));
+      }
+      if (alive) {
+        alive = cl::wait(sm::smem_u32(&ex.bar[s]), (step >> 1) & 1, a.latch);
+        if (alive && threadIdx.x == 0)  // the slot's next use, two steps on
+          sm::mbar_arrive_expect_tx(&ex.bar[s], (uint32_t)(a.K * LPR * 16));
+      }
+      for (int r = 0; r < a.K; ++r) {
+        if (r == (int)rank) enter = carry;
+        const float4 v = ex.slot[s][r][lane_c];
+        carry = fma2(f2(v.x, v.y), carry, f2(v.z, v.w));
+      }
+    } else {
+      carry = block.of(carry);
+    }
+    return enter;
+  }
+  __device__ __forceinline__ void close(F2 carry) {
+    if (a.last && rank == 0 && warp == 0 && run == 0) keep(a.last + bh * a.D + c, carry);
+    if constexpr (CLUSTER) cl::sync();  // no block leaves while others may still send to it
+  }
+};
+
+template <typename T, int LPR, int R, int STAGES, int MAXK, bool COMP, bool CLUSTER, int LOAD>
+__global__ void __launch_bounds__(kNT, 2) scan_fwd_kernel(const Args a, const __grid_constant__ Maps maps) {
+  typedef Block<T, LPR, R, 2, STAGES, MAXK, CLUSTER, LOAD> B;
+  extern __shared__ __align__(128) char stage[];
+  __shared__ float4 tot[2][kWarps][LPR];
+  __shared__ __align__(16) typename B::Ex ex;
+  __shared__ uint64_t full[STAGES];
+  B b(a, stage, full, ex);
+  F2 carry = b.state(a.first);
+  const size_t kept_rows = b.bh * (size_t)((a.T + (long long)kKeep - 1) / kKeep);
+  auto tile_of = [&](int step) { return ((long long)step * a.K + b.rank) * B::TILE; };
+  for (int s = 0; s < STAGES; ++s) b.prefetch(maps, s, tile_of(s));
 
   for (int step = 0; step < a.steps; ++step) {
-    cl::copy_wait<kStages - 1>();
-    float ai[R][VEC], bi[R][VEC];
-    Pair<VEC> p, warp_all;
+    b.arrived(step);
+    F2 av[R], bv[R];
+    Pair p, warp_all;
     p.identity();
 #pragma unroll
     for (int i = 0; i < R; ++i) {  // tokens behind the end have g = x = 0: they leave the state as it is
-      const Pack<T, VEC> pg = *reinterpret_cast<const Pack<T, VEC>*>(place(step, 0, i));
-      const Pack<T, VEC> px = *reinterpret_cast<const Pack<T, VEC>*>(place(step, 1, i));
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        float rest;
-        ai[i][j] = decay<T>(pg.get(j), &rest);
-        bi[i][j] = COMP ? rest * px.get(j) : px.get(j);
-        p.H[j] = fmaf(ai[i][j], p.H[j], bi[i][j]);
-        p.A[j] *= ai[i][j];
-      }
+      F2 rest;
+      const F2 x = Two<T>::wide(b.value(step, 1, i));
+      av[i] = decay<T, COMP>(Two<T>::wide(b.value(step, 0, i)), &rest);
+      bv[i] = COMP ? mul2(rest, x) : x;
+      p.H = fma2(av[i], p.H, bv[i]);
+      p.A = mul2(p.A, av[i]);
     }
-    prefetch(step + kStages);
-    join_warp<VEC, LPR, false>(p, warp_all, at.run_in_warp);
-    if (at.run_in_warp == 0) {
-      float* t = tot[step & 1][at.warp][at.lane_c];
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) t[j] = warp_all.A[j], t[VEC + j] = warp_all.H[j];
-    }
+    join_warp<LPR, false>(p, warp_all, b.run);
+    if (b.run == 0)
+      tot[step & 1][b.warp][b.lane_c] = make_float4(lo(warp_all.A), hi(warp_all.A), lo(warp_all.H), hi(warp_all.H));
     __syncthreads();
-    Pair<VEC> before, block;  // the block's warps in front of this one; all of them
+    b.prefetch(maps, step + STAGES, tile_of(step + STAGES));
+    Pair before, block;  // the block's warps in front of this one; all of them
+    before.identity();
     block.identity();
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      if (w == at.warp) before = block;
-      Pair<VEC> n;
-      const float* t = tot[step & 1][w][at.lane_c];
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) n.A[j] = t[j], n.H[j] = t[VEC + j];
+      const float4 v = tot[step & 1][w][b.lane_c];
+      Pair n;
+      n.A = f2(v.x, v.y), n.H = f2(v.z, v.w);
+      if (w < b.warp) before.then(n);
       block.then(n);
     }
-    float h[VEC];
-    if constexpr (CLUSTER) {
-      exchange(ex, block, carry, h, step, a.K, at.rank, at.warp, at.run_in_warp, at.lane_c, alive, a.latch);
-    } else {
+    F2 h = p.of(before.of(b.exchange(block, carry, step)));
+    const long long t0 = tile_of(step) + b.first_row();
+    if (a.hc && t0 < a.T && t0 % kKeep == 0) b.keep(a.hc + (kept_rows + (size_t)(t0 / kKeep)) * a.D + b.c, h);
+    if (a.out0 && b.mine0) {
+      size_t at = b.row(t0);
+      if (t0 + R <= a.T) {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        h[j] = carry[j];
-        carry[j] = fmaf(block.A[j], carry[j], block.H[j]);
+        for (int i = 0; i < R; ++i, at += a.D) {
+          h = fma2(av[i], h, bv[i]);
+          b.store(a.out0, at, h);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < R; ++i, at += a.D) {
+          h = fma2(av[i], h, bv[i]);
+          if (t0 + i < a.T) b.store(a.out0, at, h);
+        }
       }
-    }
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) h[j] = fmaf(p.A[j], fmaf(before.A[j], h[j], before.H[j]), p.H[j]);
-    const long long t0 = first_token(step);
-    if (a.hc && mine && t0 < a.T && t0 % kKeep == 0) {
-      const size_t n = (at.bh * (size_t)((a.T + (long long)kKeep - 1) / kKeep) + (size_t)(t0 / kKeep)) * a.D + at.c;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) a.hc[n + j] = h[j];
-    }
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      Pack<T, VEC> out;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        h[j] = fmaf(ai[i][j], h[j], bi[i][j]);
-        out.set(j, h[j]);
-      }
-      if (a.o && mine && t0 + i < a.T) out.store((T*)a.o + base + (size_t)(t0 + i) * a.D);
     }
   }
-  if (a.last && mine && at.rank == 0 && at.warp == 0 && at.run_in_warp == 0)
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) a.last[at.bh * a.D + at.c + j] = carry[j];
-  if constexpr (CLUSTER) cl::sync();  // no block leaves while others may still send to it
+  b.close(carry);
 }
 
-template <typename T, int VEC, int LPR, int R, bool COMP, bool CLUSTER>
-__global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(const Args a) {
-  constexpr int NT = kWarps * 32, RUNS = 32 / LPR, TILE = kWarps * RUNS * R, PIECE = VEC * (int)sizeof(T);
-  static_assert(TILE % kKeep == 0, "every tile starts at a kept state");
-  extern __shared__ __align__(16) char stage[];  // [kStages][3][R][NT] pieces, then [kStages][VEC][NT] floats
-  __shared__ __align__(16) float tot[2][kWarps][LPR][3 * VEC];
-  __shared__ __align__(16) Exchange<VEC, CLUSTER ? LPR : 1> ex;
-  float* kept = reinterpret_cast<float*>(stage + kStages * 3 * R * NT * PIECE);
-  const Place<VEC, LPR> at(a, CLUSTER);
-  if constexpr (CLUSTER) open_exchange(ex, a.K);
-  const T *g = (const T*)a.g, *x = (const T*)a.x, *dO = (const T*)a.dO;
-  const bool mine = at.c < a.D;
-  const size_t base = at.bh * (size_t)a.T * a.D + (mine ? at.c : 0);
-  const size_t kept_rows = at.bh * (size_t)((a.T + (long long)kKeep - 1) / kKeep);
-  float carry[VEC];  // e behind the tiles still to come
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) carry[j] = mine && a.first ? a.first[at.bh * a.D + at.c + j] : 0.f;
-  bool alive = true;
-
-  auto tile_token = [&](int step) {  // negative in front of the sequence (the last step of some ranks)
-    return ((long long)a.tiles - 1 - ((long long)step * a.K + at.rank)) * TILE;
+template <typename T, int LPR, int R, int STAGES, int MAXK, bool COMP, bool CLUSTER, int LOAD>
+__global__ void __launch_bounds__(kNT, 2) scan_bwd_kernel(const Args a, const __grid_constant__ Maps maps) {
+  typedef Block<T, LPR, R, 3, STAGES, MAXK, CLUSTER, LOAD> B;
+  static_assert(B::TILE % kKeep == 0, "every tile starts at a kept state");
+  extern __shared__ __align__(128) char stage[];
+  __shared__ float4 tot[2][kWarps][LPR];   // A and the forward H of every warp
+  __shared__ float2 tot_e[2][kWarps][LPR]; // the reverse E
+  __shared__ __align__(16) typename B::Ex ex;
+  __shared__ uint64_t full[STAGES];
+  B b(a, stage, full, ex);
+  F2 carry = b.state(a.first);  // e behind the tiles still to come
+  const size_t kept_rows = b.bh * (size_t)((a.T + (long long)kKeep - 1) / kKeep);
+  // Negative in front of the sequence (the last step of some ranks).
+  auto tile_of = [&](int step) { return ((long long)a.tiles - 1 - ((long long)step * a.K + b.rank)) * B::TILE; };
+  auto kept_state = [&](int step) {
+    const long long tile = tile_of(step);
+    if (step >= a.steps || tile < 0) return f2(0.f);
+    const float* p = a.hc_in + (kept_rows + (size_t)(tile / kKeep)) * a.D + b.c;
+    return f2(b.mine0 ? p[0] : 0.f, b.mine1 ? p[1] : 0.f);
   };
-  auto place = [&](int step, int which, int i) {
-    return stage + ((((step % kStages) * 3 + which) * R + i) * NT + threadIdx.x) * PIECE;
-  };
-  auto keep_at = [&](int step, int j) { return kept + ((step % kStages) * VEC + j) * NT + threadIdx.x; };
-  auto prefetch = [&](int step) {
-    if (step < a.steps) {
-      const long long tile = tile_token(step), t0 = tile + (at.warp * RUNS + at.run_in_warp) * R;
-      const bool real = mine && tile >= 0;
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const bool in = real && t0 + i < a.T;
-        const size_t p = in ? base + (size_t)(t0 + i) * a.D : 0;
-        fetch<T, VEC>(place(step, 0, i), g + p, in);
-        fetch<T, VEC>(place(step, 1, i), x + p, in);
-        fetch<T, VEC>(place(step, 2, i), dO + p, in);
-      }
-      const size_t n = real ? (kept_rows + (size_t)(tile / kKeep)) * a.D + at.c : 0;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j)
-        cl::copy_async<4>(gla::sm100::smem_u32(keep_at(step, j)), a.hc_in + (real ? n + j : 0), real);
-    }
-    cl::copy_commit();
-  };
-  for (int s = 0; s < kStages; ++s) prefetch(s);
+  for (int s = 0; s < STAGES; ++s) b.prefetch(maps, s, tile_of(s));
+  F2 kept_next = kept_state(0);
 
   for (int step = 0; step < a.steps; ++step) {
-    cl::copy_wait<kStages - 1>();
-    float ai[R][VEC], ri[COMP ? R : 1][VEC];  // a, and 1 - a where it is needed
-    Pair<VEC> f, e, warp_f, warp_e;           // forward and reverse action of the run
+    F2 h = kept_next;  // becomes the state that enters this run
+    kept_next = kept_state(step + 1);
+    b.arrived(step);
+    F2 av[R], rv[COMP ? R : 1];  // a, and 1 - a where it is needed
+    typename Two<T>::Raw xr[R], dr[R];
+    Pair f, e, warp_f, warp_e;  // forward and reverse action of the run
     f.identity();
     e.identity();
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      const Pack<T, VEC> pg = *reinterpret_cast<const Pack<T, VEC>*>(place(step, 0, i));
-      const Pack<T, VEC> px = *reinterpret_cast<const Pack<T, VEC>*>(place(step, 1, i));
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        float rest;
-        ai[i][j] = decay<T>(pg.get(j), &rest);
-        if constexpr (COMP) ri[i][j] = rest;
-        f.H[j] = fmaf(ai[i][j], f.H[j], COMP ? rest * px.get(j) : px.get(j));
-        f.A[j] *= ai[i][j];
+      F2 rest;
+      av[i] = decay<T, COMP>(Two<T>::wide(b.value(step, 0, i)), &rest);
+      xr[i] = b.value(step, 1, i);
+      dr[i] = b.value(step, 2, i);
+      F2 in = Two<T>::wide(xr[i]);
+      if constexpr (COMP) {
+        rv[i] = rest;
+        in = mul2(rest, in);
       }
+      f.H = fma2(av[i], f.H, in);
+      f.A = mul2(f.A, av[i]);
     }
 #pragma unroll
-    for (int i = R - 1; i >= 0; --i) {
-      const Pack<T, VEC> pd = *reinterpret_cast<const Pack<T, VEC>*>(place(step, 2, i));
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) e.H[j] = ai[i][j] * (pd.get(j) + e.H[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) e.A[j] = f.A[j];
-    join_warp<VEC, LPR, false>(f, warp_f, at.run_in_warp);
-    join_warp<VEC, LPR, true>(e, warp_e, at.run_in_warp);
-    if (at.run_in_warp == 0) {
-      float* t = tot[step & 1][at.warp][at.lane_c];
-#pragma unroll
-      for (int j = 0; j < VEC; ++j)
-        t[j] = warp_f.A[j], t[VEC + j] = warp_f.H[j], t[2 * VEC + j] = warp_e.H[j];
+    for (int i = R - 1; i >= 0; --i) e.H = mul2(av[i], add2(Two<T>::wide(dr[i]), e.H));
+    e.A = f.A;
+    join_warp<LPR, false>(f, warp_f, b.run);
+    join_warp<LPR, true>(e, warp_e, b.run);
+    if (b.run == 0) {
+      tot[step & 1][b.warp][b.lane_c] = make_float4(lo(warp_f.A), hi(warp_f.A), lo(warp_f.H), hi(warp_f.H));
+      tot_e[step & 1][b.warp][b.lane_c] = make_float2(lo(warp_e.H), hi(warp_e.H));
     }
     __syncthreads();
-    float h[VEC];  // the state that enters this run
-    Pair<VEC> behind, block;
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) h[j] = *keep_at(step, j);
-#pragma unroll
-    for (int w = 0; w < kWarps - 1; ++w) {
-      const float* t = tot[step & 1][w][at.lane_c];
-      if (w < at.warp)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) h[j] = fmaf(t[j], h[j], t[VEC + j]);
-    }
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) h[j] = fmaf(f.A[j], h[j], f.H[j]);
+    b.prefetch(maps, step + STAGES, tile_of(step + STAGES));
+    Pair behind, block;
+    behind.identity();
     block.identity();
 #pragma unroll
     for (int w = kWarps - 1; w >= 0; --w) {
-      if (w == at.warp) behind = block;
-      Pair<VEC> n;
-      const float* t = tot[step & 1][w][at.lane_c];
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) n.A[j] = t[j], n.H[j] = t[2 * VEC + j];
+      const float4 v = tot[step & 1][w][b.lane_c];
+      const float2 r = tot_e[step & 1][w][b.lane_c];
+      Pair n;
+      n.A = f2(v.x, v.y), n.H = f2(r.x, r.y);
+      if (w > b.warp) behind.then(n);
       block.then(n);
     }
-    float back[VEC];
-    if constexpr (CLUSTER) {
-      exchange(ex, block, carry, back, step, a.K, at.rank, at.warp, at.run_in_warp, at.lane_c, alive, a.latch);
-    } else {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        back[j] = carry[j];
-        carry[j] = fmaf(block.A[j], carry[j], block.H[j]);
+    for (int w = 0; w < kWarps - 1; ++w) {
+      if (w < b.warp) {
+        const float4 v = tot[step & 1][w][b.lane_c];
+        h = fma2(f2(v.x, v.y), h, f2(v.z, v.w));
       }
     }
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) back[j] = fmaf(e.A[j], fmaf(behind.A[j], back[j], behind.H[j]), e.H[j]);
-    float hp[R][VEC];  // the states before the run's tokens
+    h = f.of(h);
+    F2 back = e.of(behind.of(b.exchange(block, carry, step)));
+    F2 hp[R];  // the states before the run's tokens (less x for the complement)
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      const Pack<T, VEC> px = *reinterpret_cast<const Pack<T, VEC>*>(place(step, 1, i));
+      const F2 in = Two<T>::wide(xr[i]);
+      hp[i] = COMP ? fma2(in, f2(-1.f), h) : h;
+      h = fma2(av[i], h, COMP ? mul2(rv[i], in) : in);
+    }
+    const long long tile = tile_of(step), t0 = tile + b.first_row();
+    const bool real = b.mine0 && tile >= 0, whole = t0 + R <= a.T;
+    size_t at = real ? b.row(t0 + R - 1) : 0;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float in = px.get(j);
-        hp[i][j] = COMP ? h[j] - in : h[j];
-        h[j] = fmaf(ai[i][j], h[j], COMP ? ri[i][j] * in : in);
+    for (int i = R - 1; i >= 0; --i, at -= a.D) {
+      const F2 d = add2(Two<T>::wide(dr[i]), back);
+      back = mul2(av[i], d);
+      if (real && (whole || t0 + i < a.T)) {
+        b.store(a.out0, at, COMP ? mul2(rv[i], d) : d);
+        b.store(a.out1, at, mul2(back, hp[i]));
       }
     }
-    const long long tile = tile_token(step), t0 = tile + (at.warp * RUNS + at.run_in_warp) * R;
-    const bool real = mine && tile >= 0;
-#pragma unroll
-    for (int i = R - 1; i >= 0; --i) {
-      const Pack<T, VEC> pd = *reinterpret_cast<const Pack<T, VEC>*>(place(step, 2, i));
-      Pack<T, VEC> og, ox;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float d = pd.get(j) + back[j];
-        back[j] = ai[i][j] * d;
-        ox.set(j, COMP ? ri[i][j] * d : d);
-        og.set(j, back[j] * hp[i][j]);
-      }
-      if (real && t0 + i < a.T) {
-        const size_t p = base + (size_t)(t0 + i) * a.D;
-        ox.store((T*)a.dx + p);
-        og.store((T*)a.dg + p);
-      }
-    }
-    prefetch(step + kStages);
   }
-  if (a.last && mine && at.rank == 0 && at.warp == 0 && at.run_in_warp == 0)
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) a.last[at.bh * a.D + at.c + j] = carry[j];
-  if constexpr (CLUSTER) cl::sync();
+  b.close(carry);
 }
 
 template <typename T, bool COMP>
@@ -478,9 +517,9 @@ __global__ void scan_step_kernel(const T* __restrict__ g, const T* __restrict__ 
                                  T* __restrict__ o, long long n) {
   const long long c = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   if (c >= n) return;
-  float rest;
-  const float a = decay<T>(ldf(g + c), &rest), in = ldf(x + c);
-  const float h = fmaf(a, S[c], COMP ? rest * in : in);
+  F2 rest;
+  const float a = lo(decay<T, COMP>(f2(ldf(g + c)), &rest)), in = ldf(x + c);
+  const float h = fmaf(a, S[c], COMP ? lo(rest) * in : in);
   S[c] = h;
   stf(o + c, h);
 }
@@ -510,39 +549,63 @@ int check_ptr(const void* p, size_t esize, bool required) {
 size_t esize(int dtype) { return dtype == GLA_DTYPE_BF16 ? 2 : 4; }
 int launched() { return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_CUDA; }
 
-constexpr int kRun = 8;          // tokens a thread
-constexpr int kFill = 148 * 2;   // blocks that run at once: two an SM
+constexpr int kFill = 148 * 2;  // blocks that run at once: two an SM
+
+// Tensor map over [BH, T, D] with boxes of (box_d, box_t) values; everything outside reads as zeros.
+bool make_map(CUtensorMap* m, const void* base, long long BH, int T, int D, int box_d, int box_t, bool is_bf16) {
+  auto fn = gla::fast::encode_fn();
+  if (!fn) return false;
+  const cuuint64_t es = is_bf16 ? 2 : 4;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)T, (cuuint64_t)BH};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * es, (cuuint64_t)D * es * (cuuint64_t)T};
+  const cuuint32_t box[3] = {(cuuint32_t)box_d, (cuuint32_t)box_t, 1}, one[3] = {1, 1, 1};
+  return fn(m, is_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(base),
+            dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 // Launches one variant; K blocks of a cluster share a slab.  K is the largest power of two that keeps all blocks
 // running at once, and no more than there are tiles.
-template <typename T, int VEC, int LPR, bool COMP, bool BWD>
+template <typename T, int LPR, int LOAD, bool COMP, bool BWD>
 int launch(Args a, long long BH, cudaStream_t st) {
-  constexpr int TILE = kWarps * (32 / LPR) * kRun, PIECE = VEC * (int)sizeof(T);
-  constexpr int SMEM = kStages * (BWD ? 3 * kRun * PIECE + 4 * VEC : 2 * kRun * PIECE) * kWarps * 32;
-  a.slabs = (a.D + LPR * VEC - 1) / (LPR * VEC);
-  a.tiles = (int)(((long long)a.T + TILE - 1) / TILE);
+  constexpr int R = BWD || LPR < 32 || sizeof(T) == 4 ? 8 : 16;     // tokens a thread: a tile of g is 16 KB or less
+  constexpr int STAGES = BWD && sizeof(T) == 4 && LPR == 32 ? 2 : 3;  // two blocks of an SM have 227 KB
+  constexpr int MAXK = LPR < 32 ? 16 : BWD && sizeof(T) == 4 ? 4 : 8;  // likewise: the slots take K LPR 32 bytes
+  typedef Block<T, LPR, R, BWD ? 3 : 2, STAGES, MAXK, true, LOAD> B;
+  constexpr int SMEM = STAGES * B::STAGE;
+  a.slabs = (a.D + B::CW - 1) / B::CW;
+  a.tiles = (int)(((long long)a.T + B::TILE - 1) / B::TILE);
   const long long cols = BH * a.slabs;
   int K = 1;
-  while (K < kMaxK && K * 2 <= a.tiles && cols * K * 2 <= kFill) K *= 2;
+  while (K < MAXK && K * 2 <= a.tiles && cols * K * 2 <= kFill) K *= 2;
   a.K = K;
   a.steps = (a.tiles + K - 1) / K;
-  void (*kernel)(const Args);
+  Maps maps;
+  if (LOAD == kTma && a.T > 0)
+    for (int n = 0; n < (BWD ? 3 : 2); ++n)
+      if (!make_map(&maps.m[n], a.in[n], BH, a.T, a.D, B::CW, B::TILE, sizeof(T) == 2)) return GLA_ERR_CUDA;
+  void (*kernel)(const Args, const Maps);
   if constexpr (BWD)
-    kernel = K > 1 ? scan_bwd_kernel<T, VEC, LPR, kRun, COMP, true> : scan_bwd_kernel<T, VEC, LPR, kRun, COMP, false>;
+    kernel = K > 1 ? scan_bwd_kernel<T, LPR, R, STAGES, MAXK, COMP, true, LOAD>
+                   : scan_bwd_kernel<T, LPR, R, STAGES, MAXK, COMP, false, LOAD>;
   else
-    kernel = K > 1 ? scan_fwd_kernel<T, VEC, LPR, kRun, COMP, true> : scan_fwd_kernel<T, VEC, LPR, kRun, COMP, false>;
-  // Shared memory above 48 KB is asked for once per device (and kernel).
-  static std::atomic<unsigned long long> allowed[2] = {};
+    kernel = K > 1 ? scan_fwd_kernel<T, LPR, R, STAGES, MAXK, COMP, true, LOAD>
+                   : scan_fwd_kernel<T, LPR, R, STAGES, MAXK, COMP, false, LOAD>;
+  // Shared memory above 48 KB and clusters of 16 are asked for once per device and kernel.
+  static std::atomic<bool> done[2][64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return GLA_ERR_CUDA;
-  const unsigned long long bit = 1ull << (dev & 63);
-  if (!(allowed[K > 1].load(std::memory_order_relaxed) & bit) || dev > 63) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess) return GLA_ERR_CUDA;
-    allowed[K > 1].fetch_or(bit, std::memory_order_relaxed);
+  if (dev < 0 || dev > 63 || !done[K > 1][dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess ||
+        (MAXK > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)) {
+      (void)cudaGetLastError();
+      return GLA_ERR_CUDA;
+    }
+    if (dev >= 0 && dev < 64) done[K > 1][dev].store(true, std::memory_order_release);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(cols * K));
-  cfg.blockDim = dim3(kWarps * 32);
+  cfg.blockDim = dim3(kNT);
   cfg.dynamicSmemBytes = SMEM;
   cfg.stream = st;
   cudaLaunchAttribute attr;
@@ -551,54 +614,46 @@ int launch(Args a, long long BH, cudaStream_t st) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = K > 1 ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, kernel, (const Args)a) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, kernel, (const Args)a, (const Maps)maps) != cudaSuccess) {
     (void)cudaGetLastError();
     return GLA_ERR_CUDA;
   }
   return GLA_OK;
 }
 
-// Slabs: rows of 32 pieces (8 bytes each) make the longest requests; where even clusters of them leave most SMs
-// idle, slabs of 8 pieces, whose tiles are four times as long, give four times the blocks.
-template <typename T, int VEC, bool COMP, bool BWD>
+// Slabs of 64 channels make rows of 128 bytes or more; where even clusters of them leave most SMs idle, slabs of 16
+// channels, in tiles of 256 tokens and clusters of up to 16, give more blocks.
+template <typename T, int LOAD, bool COMP, bool BWD>
 int choose(const Args& a, long long BH, cudaStream_t st) {
-  const long long wide = BH * ((a.D + 32 * VEC - 1) / (32 * VEC));
-  const long long tiles = ((long long)a.T + 63) / 64;
-  const long long blocks = wide * (tiles < kMaxK ? tiles : kMaxK);
-  if (blocks * 2 <= kFill && tiles > kMaxK) return launch<T, VEC, 8, COMP, BWD>(a, BH, st);
-  return launch<T, VEC, 32, COMP, BWD>(a, BH, st);
+  const long long wide = BH * ((a.D + 63) / 64), tiles = ((long long)a.T + 63) / 64;
+  if (wide * (tiles < 8 ? tiles : 8) * 2 <= kFill && tiles > 8) return launch<T, 8, LOAD, COMP, BWD>(a, BH, st);
+  return launch<T, 32, LOAD, COMP, BWD>(a, BH, st);
 }
 
 template <bool BWD>
-int run(const Args& a, long long BH, int input, int dtype, cudaStream_t st) {
+int run(Args a, long long BH, int input, int dtype, cudaStream_t st) {
   const size_t es = esize(dtype);
-  // The widest piece that divides a row and every address: at most 8 bytes, or 4 in the backward, whose third
-  // array and reverse pairs would otherwise leave room for one block an SM.
-  int vec = (int)((BWD ? 4 : 8) / es);
-  auto fits = [&](int v) {
-    if (a.D % v != 0) return false;
-    for (const void* p : {a.g, a.x, a.dO, (const void*)a.o, (const void*)a.dg, (const void*)a.dx})
-      if (!gla::aligned_to(p, v * es)) return false;
+  auto fits = [&](size_t bytes) {
+    if (a.D * es % bytes != 0) return false;
+    for (const void* p : {a.in[0], a.in[1], a.in[2], (const void*)a.out0, (const void*)a.out1})
+      if (!gla::aligned_to(p, bytes)) return false;
     return true;
   };
-  while (vec > 1 && !fits(vec)) vec /= 2;
+  // TMA counts tokens and heads in 32 bits and strides up to 2^40 bytes.
+  const bool tma = fits(16) && a.T < (1 << 30) && (double)a.D * es * a.T < 1099511627776.0;
+  a.pairs = fits(2 * es);
   const bool comp = input == GLA_SCAN_COMPLEMENT;
-#define SCAN_CHOOSE(TYPE, VEC) (comp ? choose<TYPE, VEC, true, BWD>(a, BH, st) : choose<TYPE, VEC, false, BWD>(a, BH, st))
-  if (dtype == GLA_DTYPE_BF16) {
-    if constexpr (!BWD)
-      if (vec == 4) return SCAN_CHOOSE(bf16, 4);
-    return vec == 2 ? SCAN_CHOOSE(bf16, 2) : SCAN_CHOOSE(bf16, 1);
-  }
-  if constexpr (!BWD)
-    if (vec == 2) return SCAN_CHOOSE(float, 2);
-  return SCAN_CHOOSE(float, 1);
+#define SCAN_CHOOSE(TYPE)                                                                                             \
+  (tma ? (comp ? choose<TYPE, kTma, true, BWD>(a, BH, st) : choose<TYPE, kTma, false, BWD>(a, BH, st))                \
+       : (comp ? choose<TYPE, kByThread, true, BWD>(a, BH, st) : choose<TYPE, kByThread, false, BWD>(a, BH, st)))
+  return dtype == GLA_DTYPE_BF16 ? SCAN_CHOOSE(bf16) : SCAN_CHOOSE(float);
 #undef SCAN_CHOOSE
 }
 
 int fwd(const void* g, const void* x, const float* h0, void* o, float* hT, float* hc, int B, int H, int T, int D,
         int input, int dtype, cudaStream_t st) {
   Args a = {};
-  a.g = g, a.x = x, a.first = h0, a.o = o, a.last = hT, a.hc = hc;
+  a.in[0] = g, a.in[1] = x, a.first = h0, a.out0 = o, a.last = hT, a.hc = hc;
   a.T = T, a.D = D, a.latch = gla::device_error_latch();
   return run<false>(a, (long long)B * H, input, dtype, st);
 }
@@ -645,7 +700,7 @@ extern "C" int gla_scan_bwd(const void* g, const void* x, const float* h0, const
     hc = static_cast<const float*>(workspace);
   }
   Args a = {};
-  a.g = g, a.x = x, a.dO = dO, a.hc_in = hc, a.first = dhT, a.dg = dg, a.dx = dx, a.last = dh0;
+  a.in[0] = g, a.in[1] = x, a.in[2] = dO, a.hc_in = hc, a.first = dhT, a.out0 = dx, a.out1 = dg, a.last = dh0;
   a.T = T, a.D = D, a.latch = gla::device_error_latch();
   return run<true>(a, (long long)B * H, input, dtype, st);
 }
