@@ -32,97 +32,58 @@
 #include "../../include/gla.h"
 #include "fast_path.cuh"
 #include "fused_common.cuh"
+#include "pair_math.cuh"
 #include "scan_cluster.cuh"
 #include "vec.cuh"
 
 namespace {
 
+using gla::add2;
 using gla::bf16;
+using gla::f2;
+using gla::F2;
+using gla::fma2;
+using gla::hi;
 using gla::ldf;
+using gla::lo;
+using gla::mul2;
 using gla::stf;
+using gla::Two;
 namespace cl = gla::cluster;
 namespace sm = gla::sm100;
 
 constexpr int kKeep = 64;          // tokens between the kept states
-constexpr int kWarps = 8;          // warps a block
-constexpr int kNT = kWarps * 32;   // threads a block
 
-// ---- two fp32 values in a register pair -------------------------------------------------------------
-struct F2 {
-  uint64_t v;
-};
-__device__ __forceinline__ F2 f2(float lo, float hi) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ F2 f2(float x) { return f2(x, x); }
-__device__ __forceinline__ float lo(F2 a) {
-  float x, y;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v));
-  return x;
-}
-__device__ __forceinline__ float hi(F2 a) {
-  float x, y;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v));
-  return y;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
 __device__ __forceinline__ F2 shfl2(F2 a, int src) {
   return f2(__shfl_sync(0xffffffffu, lo(a), src), __shfl_sync(0xffffffffu, hi(a), src));
 }
 
-// Two neighbouring values as they lie in memory.
-template <typename T>
-struct Two;
-template <>
-struct Two<bf16> {
-  typedef uint32_t Raw;
-  static __device__ __forceinline__ F2 wide(Raw w) {
-    return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-  }
-  static __device__ __forceinline__ Raw narrow(F2 v) { return gla::fast::pack2(lo(v), hi(v)); }
-};
-template <>
-struct Two<float> {
-  typedef uint64_t Raw;
-  static __device__ __forceinline__ F2 wide(Raw w) { return F2{w}; }
-  static __device__ __forceinline__ Raw narrow(F2 v) { return v.v; }
-};
-
 // a = exp g and, with REST, 1 - a.  Near g = 0 both come from exp g - 1 = g (1 + g/2 (1 + g/3 (...))), so that
-// neither the 1 - a of a slow gate nor a long product of a's loses its leading digits; the series ends five terms
-// in, where |g| < 1/8 leaves a relative error below g^5/720 < 2^-24.  Elsewhere a state forgets within a few dozen
-// tokens, and the exponential's own error (2^-22 for the approximate one at bf16) has no time to add up.
+// neither the 1 - a of a slow gate nor a long product of a's loses its leading digits.  For a alone three terms do up
+// to |g| = 1/32 (what is left out, g^4/24, is below 2^-24); 1 - a takes five terms up to 1/8, where 1 - e^g keeps
+// enough digits.  Elsewhere a state forgets within a few dozen tokens, and the exponential's own error (2^-22 for the
+// approximate one at bf16) has no time to add up.
 template <typename T, bool REST>
 __device__ __forceinline__ F2 decay(F2 g, F2* rest) {
-  F2 t = fma2(g, f2(1.f / 120.f), f2(1.f / 24.f));
-  t = fma2(g, t, f2(1.f / 6.f));
+  F2 t;
+  if constexpr (REST) {
+    t = fma2(g, f2(1.f / 120.f), f2(1.f / 24.f));
+    t = fma2(g, t, f2(1.f / 6.f));
+  } else {
+    t = f2(1.f / 6.f);
+  }
   t = fma2(g, t, f2(0.5f));
   t = fma2(g, t, f2(1.f));
   const F2 near = fma2(t, g, f2(1.f));
   F2 far;
   if constexpr (sizeof(T) == 2) {
     const F2 y = mul2(g, f2(gla::fast::kLog2e));
-    far = f2(gla::fast::ex2(lo(y)), gla::fast::ex2(hi(y)));
+    far = f2(gla::fast_ex2(lo(y)), gla::fast_ex2(hi(y)));
   } else {
     far = f2(expf(lo(g)), expf(hi(g)));
   }
-  const bool s0 = fabsf(lo(g)) < 0.125f, s1 = fabsf(hi(g)) < 0.125f;
+  constexpr float kNear = REST ? 0.125f : 0.03125f;
+  const bool s0 = fabsf(lo(g)) < kNear, s1 = fabsf(hi(g)) < kNear;
   if constexpr (REST) {
     const F2 rn = mul2(t, mul2(g, f2(-1.f))), rf = fma2(far, f2(-1.f), f2(1.f));
     *rest = f2(s0 ? lo(rn) : lo(rf), s1 ? hi(rn) : hi(rf));
@@ -199,9 +160,9 @@ struct Exchange {
   uint64_t bar[2];
 };
 
-template <typename T, int LPR, int R, int NIN, int STAGES, int MAXK, bool CLUSTER, int LOAD>
+template <typename T, int W, int LPR, int R, int NIN, int STAGES, int MAXK, bool CLUSTER, int LOAD>
 struct Block {
-  static constexpr int RUNS = 32 / LPR, TILE = kWarps * RUNS * R, CW = 2 * LPR;
+  static constexpr int RUNS = 32 / LPR, TILE = W * RUNS * R, CW = 2 * LPR;
   static constexpr int ROW = CW * (int)sizeof(T), ARRAY = TILE * ROW, STAGE = NIN * ARRAY;
   typedef typename Two<T>::Raw Raw;
   typedef Exchange<CLUSTER ? LPR : 1, CLUSTER ? MAXK : 1> Ex;
@@ -250,6 +211,41 @@ struct Block {
     if (mine1) p[1] = hi(v);
   }
 
+  // This thread's values of the R tokens from t0 (zeros from T on and behind the last channel; INSIDE: none of those).
+  template <bool INSIDE>
+  __device__ __forceinline__ void fetch(char* at, long long t0) const {
+    constexpr int ES = (int)sizeof(T);
+#pragma unroll
+    for (int n = 0; n < NIN; ++n) {
+      const T* src = (const T*)a.in[n];
+      const T* p = src + (INSIDE || (mine0 && t0 < a.T) ? row(t0) : 0);
+      char* dst = at + n * ARRAY + first_row() * ROW + lane_c * 2 * ES;
+      if (a.pairs || ES == 4) {
+#pragma unroll
+        for (int i = 0; i < R; ++i, p += a.D, dst += ROW) {
+          const bool in0 = INSIDE || (mine0 && t0 + i < a.T), in1 = INSIDE || (in0 && mine1);
+          if (a.pairs) {
+            cl::copy_async<2 * ES>(sm::smem_u32(dst), in0 ? p : src, in0);
+          } else {
+            cl::copy_async<4>(sm::smem_u32(dst), in0 ? p : src, in0);
+            cl::copy_async<4>(sm::smem_u32(dst + 4), in1 ? p + 1 : src, in1);
+          }
+        }
+      } else {  // odd rows of bf16: nothing asynchronous is that narrow
+        uint32_t v[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i, p += a.D) {
+          const bool in0 = INSIDE || (mine0 && t0 + i < a.T), in1 = INSIDE || (in0 && mine1);
+          const unsigned short* w = reinterpret_cast<const unsigned short*>(p);
+          v[i] = in0 ? (uint32_t)__ldg(w) : 0u;
+          if (in1) v[i] |= (uint32_t)__ldg(w + 1) << 16;
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) *reinterpret_cast<uint32_t*>(dst + i * ROW) = v[i];
+      }
+    }
+  }
+
   // Starts the copy of the tile whose first token is `tile` (a tile outside the sequence reads as zeros) for
   // step `step`; with kTma by one thread, when all threads have taken the values that lay there.
   __device__ __forceinline__ void prefetch(const Maps& maps, int step, long long tile) {
@@ -264,28 +260,8 @@ struct Block {
     } else {
       if (step < a.steps) {
         const long long t0 = tile + first_row();
-        char* p = at + first_row() * ROW + lane_c * 2 * sizeof(T);
-#pragma unroll
-        for (int n = 0; n < NIN; ++n)
-#pragma unroll
-          for (int i = 0; i < R; ++i, p += ROW) {
-            if (i == 0) p = at + n * ARRAY + first_row() * ROW + lane_c * 2 * sizeof(T);
-            const bool in = tile >= 0 && t0 + i < a.T;
-            const T* src = (const T*)a.in[n] + (in && mine0 ? row(t0 + i) : 0);
-            if (a.pairs) {
-              cl::copy_async<2 * (int)sizeof(T)>(sm::smem_u32(p), src, in && mine0);
-            } else if constexpr (sizeof(T) == 4) {
-              cl::copy_async<4>(sm::smem_u32(p), src, in && mine0);
-              cl::copy_async<4>(sm::smem_u32(p + 4), in && mine1 ? src + 1 : src, in && mine1);
-            } else {
-              T v0, v1;
-              stf(&v0, 0.f), stf(&v1, 0.f);
-              if (in && mine0) v0 = src[0];
-              if (in && mine1) v1 = src[1];
-              reinterpret_cast<T*>(p)[0] = v0;
-              reinterpret_cast<T*>(p)[1] = v1;
-            }
-          }
+        if (mine1 && tile >= 0 && t0 + R <= a.T) fetch<true>(at, t0);
+        else fetch<false>(at, tile < 0 ? a.T : t0);
       }
       cl::copy_commit();
     }
@@ -301,8 +277,7 @@ struct Block {
     return *reinterpret_cast<const Raw*>(stage + (step % STAGES) * STAGE + which * ARRAY + (first_row() + i) * ROW +
                                          lane_c * 2 * sizeof(T));
   }
-  __device__ __forceinline__ void store(void* out, size_t at, F2 v) const {
-    T* p = (T*)out + at;
+  __device__ __forceinline__ void store(T* p, F2 v) const {
     if (LOAD == kTma || a.pairs) {
       *reinterpret_cast<Raw*>(p) = Two<T>::narrow(v);
     } else {
@@ -321,7 +296,7 @@ struct Block {
       const int s = step & 1;
       if (run == 0) {
         const float v[4] = {lo(block.A), hi(block.A), lo(block.H), hi(block.H)};
-        for (int r = warp; r < a.K; r += kWarps)
+        for (int r = warp; r < a.K; r += W)
           cl::store_async(cl::peer(sm::smem_u32(&ex.slot[s][rank][lane_c]), r), v, cl::peer(sm::smem_u32(&ex.bar[s]), r));
       }
       if (alive) {
@@ -345,11 +320,11 @@ struct Block {
   }
 };
 
-template <typename T, int LPR, int R, int STAGES, int MAXK, bool COMP, bool CLUSTER, int LOAD>
-__global__ void __launch_bounds__(kNT, 2) scan_fwd_kernel(const Args a, const __grid_constant__ Maps maps) {
-  typedef Block<T, LPR, R, 2, STAGES, MAXK, CLUSTER, LOAD> B;
+template <typename T, int W, int LPR, int R, int STAGES, int MINB, int MAXK, bool COMP, bool CLUSTER, int LOAD>
+__global__ void __launch_bounds__(W * 32, MINB) scan_fwd_kernel(const Args a, const __grid_constant__ Maps maps) {
+  typedef Block<T, W, LPR, R, 2, STAGES, MAXK, CLUSTER, LOAD> B;
   extern __shared__ __align__(128) char stage[];
-  __shared__ float4 tot[2][kWarps][LPR];
+  __shared__ float4 tot[2][W][LPR];
   __shared__ __align__(16) typename B::Ex ex;
   __shared__ uint64_t full[STAGES];
   B b(a, stage, full, ex);
@@ -381,7 +356,7 @@ __global__ void __launch_bounds__(kNT, 2) scan_fwd_kernel(const Args a, const __
     before.identity();
     block.identity();
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < W; ++w) {
       const float4 v = tot[step & 1][w][b.lane_c];
       Pair n;
       n.A = f2(v.x, v.y), n.H = f2(v.z, v.w);
@@ -392,18 +367,18 @@ __global__ void __launch_bounds__(kNT, 2) scan_fwd_kernel(const Args a, const __
     const long long t0 = tile_of(step) + b.first_row();
     if (a.hc && t0 < a.T && t0 % kKeep == 0) b.keep(a.hc + (kept_rows + (size_t)(t0 / kKeep)) * a.D + b.c, h);
     if (a.out0 && b.mine0) {
-      size_t at = b.row(t0);
+      T* out = (T*)a.out0 + b.row(t0);
       if (t0 + R <= a.T) {
 #pragma unroll
-        for (int i = 0; i < R; ++i, at += a.D) {
+        for (int i = 0; i < R; ++i, out += a.D) {
           h = fma2(av[i], h, bv[i]);
-          b.store(a.out0, at, h);
+          b.store(out, h);
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < R; ++i, at += a.D) {
+        for (int i = 0; i < R; ++i, out += a.D) {
           h = fma2(av[i], h, bv[i]);
-          if (t0 + i < a.T) b.store(a.out0, at, h);
+          if (t0 + i < a.T) b.store(out, h);
         }
       }
     }
@@ -411,13 +386,13 @@ __global__ void __launch_bounds__(kNT, 2) scan_fwd_kernel(const Args a, const __
   b.close(carry);
 }
 
-template <typename T, int LPR, int R, int STAGES, int MAXK, bool COMP, bool CLUSTER, int LOAD>
-__global__ void __launch_bounds__(kNT, 2) scan_bwd_kernel(const Args a, const __grid_constant__ Maps maps) {
-  typedef Block<T, LPR, R, 3, STAGES, MAXK, CLUSTER, LOAD> B;
+template <typename T, int W, int LPR, int R, int STAGES, int MINB, int MAXK, bool COMP, bool CLUSTER, int LOAD>
+__global__ void __launch_bounds__(W * 32, MINB) scan_bwd_kernel(const Args a, const __grid_constant__ Maps maps) {
+  typedef Block<T, W, LPR, R, 3, STAGES, MAXK, CLUSTER, LOAD> B;
   static_assert(B::TILE % kKeep == 0, "every tile starts at a kept state");
   extern __shared__ __align__(128) char stage[];
-  __shared__ float4 tot[2][kWarps][LPR];   // A and the forward H of every warp
-  __shared__ float2 tot_e[2][kWarps][LPR]; // the reverse E
+  __shared__ float4 tot[2][W][LPR];   // A and the forward H of every warp
+  __shared__ float2 tot_e[2][W][LPR]; // the reverse E
   __shared__ __align__(16) typename B::Ex ex;
   __shared__ uint64_t full[STAGES];
   B b(a, stage, full, ex);
@@ -472,7 +447,7 @@ __global__ void __launch_bounds__(kNT, 2) scan_bwd_kernel(const Args a, const __
     behind.identity();
     block.identity();
 #pragma unroll
-    for (int w = kWarps - 1; w >= 0; --w) {
+    for (int w = W - 1; w >= 0; --w) {
       const float4 v = tot[step & 1][w][b.lane_c];
       const float2 r = tot_e[step & 1][w][b.lane_c];
       Pair n;
@@ -481,7 +456,7 @@ __global__ void __launch_bounds__(kNT, 2) scan_bwd_kernel(const Args a, const __
       block.then(n);
     }
 #pragma unroll
-    for (int w = 0; w < kWarps - 1; ++w) {
+    for (int w = 0; w < W - 1; ++w) {
       if (w < b.warp) {
         const float4 v = tot[step & 1][w][b.lane_c];
         h = fma2(f2(v.x, v.y), h, f2(v.z, v.w));
@@ -498,14 +473,14 @@ __global__ void __launch_bounds__(kNT, 2) scan_bwd_kernel(const Args a, const __
     }
     const long long tile = tile_of(step), t0 = tile + b.first_row();
     const bool real = b.mine0 && tile >= 0, whole = t0 + R <= a.T;
-    size_t at = real ? b.row(t0 + R - 1) : 0;
+    size_t at = real ? b.row(t0 + R - 1) : 0;  // one offset: a pointer for each output spills the complement's values
 #pragma unroll
     for (int i = R - 1; i >= 0; --i, at -= a.D) {
       const F2 d = add2(Two<T>::wide(dr[i]), back);
       back = mul2(av[i], d);
       if (real && (whole || t0 + i < a.T)) {
-        b.store(a.out0, at, COMP ? mul2(rv[i], d) : d);
-        b.store(a.out1, at, mul2(back, hp[i]));
+        b.store((T*)a.out0 + at, COMP ? mul2(rv[i], d) : d);
+        b.store((T*)a.out1 + at, mul2(back, hp[i]));
       }
     }
   }
@@ -549,7 +524,6 @@ int check_ptr(const void* p, size_t esize, bool required) {
 size_t esize(int dtype) { return dtype == GLA_DTYPE_BF16 ? 2 : 4; }
 int launched() { return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_CUDA; }
 
-constexpr int kFill = 148 * 2;  // blocks that run at once: two an SM
 
 // Tensor map over [BH, T, D] with boxes of (box_d, box_t) values; everything outside reads as zeros.
 bool make_map(CUtensorMap* m, const void* base, long long BH, int T, int D, int box_d, int box_t, bool is_bf16) {
@@ -568,10 +542,18 @@ bool make_map(CUtensorMap* m, const void* base, long long BH, int T, int D, int 
 // running at once, and no more than there are tiles.
 template <typename T, int LPR, int LOAD, bool COMP, bool BWD>
 int launch(Args a, long long BH, cudaStream_t st) {
-  constexpr int R = BWD || LPR < 32 || sizeof(T) == 4 ? 8 : 16;     // tokens a thread: a tile of g is 16 KB or less
-  constexpr int STAGES = BWD && sizeof(T) == 4 && LPR == 32 ? 2 : 3;  // two blocks of an SM have 227 KB
+  // Forward: blocks of 4 warps, three an SM, 16 tokens a thread; one tile of g is 8 KB (16 KB fp32), so three stages
+  // of three blocks fit the 227 KB.  Blocks of 8 warps with the same tile bytes in flight pay for joining twice the
+  // warps (B=8, T=2048, C=2048 bf16: 45 against 43 us; B=1, T=32768, C=1024: 72 against 57 us), 8 tokens a thread for
+  // twice the joins an element (55 us).  Backward: the third array and the recomputed states take the registers of 8
+  // more tokens: 8 tokens a thread, 8 warps (a tile has to start at a kept state), two blocks an SM; 16 tokens a
+  // thread spill (217 against 84 us for the complement).
+  constexpr int W = BWD ? 8 : 4, MINB = BWD ? 2 : 3;
+  constexpr int R = BWD ? 8 : sizeof(T) == 4 && LPR < 32 ? 8 : 16;
+  constexpr int STAGES = BWD && sizeof(T) == 4 ? 2 : sizeof(T) == 4 && LPR == 32 ? 2 : 3;
   constexpr int MAXK = LPR < 32 ? 16 : BWD && sizeof(T) == 4 ? 4 : 8;  // likewise: the slots take K LPR 32 bytes
-  typedef Block<T, LPR, R, BWD ? 3 : 2, STAGES, MAXK, true, LOAD> B;
+  constexpr int kFill = 148 * MINB;  // blocks that run at once
+  typedef Block<T, W, LPR, R, BWD ? 3 : 2, STAGES, MAXK, true, LOAD> B;
   constexpr int SMEM = STAGES * B::STAGE;
   a.slabs = (a.D + B::CW - 1) / B::CW;
   a.tiles = (int)(((long long)a.T + B::TILE - 1) / B::TILE);
@@ -586,11 +568,11 @@ int launch(Args a, long long BH, cudaStream_t st) {
       if (!make_map(&maps.m[n], a.in[n], BH, a.T, a.D, B::CW, B::TILE, sizeof(T) == 2)) return GLA_ERR_CUDA;
   void (*kernel)(const Args, const Maps);
   if constexpr (BWD)
-    kernel = K > 1 ? scan_bwd_kernel<T, LPR, R, STAGES, MAXK, COMP, true, LOAD>
-                   : scan_bwd_kernel<T, LPR, R, STAGES, MAXK, COMP, false, LOAD>;
+    kernel = K > 1 ? scan_bwd_kernel<T, W, LPR, R, STAGES, MINB, MAXK, COMP, true, LOAD>
+                   : scan_bwd_kernel<T, W, LPR, R, STAGES, MINB, MAXK, COMP, false, LOAD>;
   else
-    kernel = K > 1 ? scan_fwd_kernel<T, LPR, R, STAGES, MAXK, COMP, true, LOAD>
-                   : scan_fwd_kernel<T, LPR, R, STAGES, MAXK, COMP, false, LOAD>;
+    kernel = K > 1 ? scan_fwd_kernel<T, W, LPR, R, STAGES, MINB, MAXK, COMP, true, LOAD>
+                   : scan_fwd_kernel<T, W, LPR, R, STAGES, MINB, MAXK, COMP, false, LOAD>;
   // Shared memory above 48 KB and clusters of 16 are asked for once per device and kernel.
   static std::atomic<bool> done[2][64];
   int dev = 0;
@@ -605,7 +587,7 @@ int launch(Args a, long long BH, cudaStream_t st) {
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(cols * K));
-  cfg.blockDim = dim3(kNT);
+  cfg.blockDim = dim3(W * 32);
   cfg.dynamicSmemBytes = SMEM;
   cfg.stream = st;
   cudaLaunchAttribute attr;
@@ -626,7 +608,7 @@ int launch(Args a, long long BH, cudaStream_t st) {
 template <typename T, int LOAD, bool COMP, bool BWD>
 int choose(const Args& a, long long BH, cudaStream_t st) {
   const long long wide = BH * ((a.D + 63) / 64), tiles = ((long long)a.T + 63) / 64;
-  if (wide * (tiles < 8 ? tiles : 8) * 2 <= kFill && tiles > 8) return launch<T, 8, LOAD, COMP, BWD>(a, BH, st);
+  if (wide * (tiles < 8 ? tiles : 8) * 2 <= 296 && tiles > 8) return launch<T, 8, LOAD, COMP, BWD>(a, BH, st);
   return launch<T, 32, LOAD, COMP, BWD>(a, BH, st);
 }
 
