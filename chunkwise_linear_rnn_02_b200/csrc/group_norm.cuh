@@ -7,16 +7,16 @@
 // (without the mean terms of dn for the RMS form; du = dy act'(u) without a gate).
 //
 // HBM-bound: one pass, a row stays packed in the registers of the lanes that share it, so x, z and dy are read once
-// and y, dx, dz written once.  The mean is subtracted before the squares are summed.  Eight values a lane (16 bytes
-// of bf16), so that the fp32 copies and, in the backward, the running sums of dw and db leave room for enough warps
-// to cover the memory's latency; the row of the next step is loaded before this one is worked on.  The arithmetic
-// goes through packed fp32 pairs.
-// A block serves one head and strides over the tokens, so that a lane keeps its channels: w and b are loaded once,
-// and the sums of dw and db stay in registers until the block ends.  They are then joined over the block's rows,
-// written as one partial row a block, and a second launch adds the partial rows in order (no atomics: the result
-// does not depend on how blocks are scheduled).
+// and y, dx, dz written once.  The mean is subtracted before the squares are summed.  What there is to save is
+// instructions (at full bandwidth a bf16 value has about 30 issue slots forward, 55 backward) and the latency of two
+// dependent row sums: 16 values a lane at bf16, so that D = 512 needs no more than a warp (8 a lane: 59 and 86 us in the
+// case below), packed fp32 pairs for the arithmetic, and the row of the next step loaded before this one is worked on.
+// A block serves one head and strides over the tokens, so that a lane keeps its channels: w and b are loaded once
+// (the backward keeps them in shared memory), and the sums of dw and db stay in registers until the block ends.  They
+// are then joined over the block's rows, written as one partial row a block, and a second launch adds the partial
+// rows in order (no atomics: the result does not depend on how blocks are scheduled).
 //
-// B=8, H=4, T=2048, D=512 bf16, gate and weights: see the two .cu files.
+// B=8, H=4, T=2048, D=512 bf16 with gate and weights: forward 43 us (4.7 TB/s), backward 77 us (4.4 TB/s).
 #pragma once
 
 #include <limits.h>
@@ -110,10 +110,12 @@ struct Row {
 
   static __device__ __forceinline__ int channel(int lane, int e) { return (lane + e / V * LANES) * V + e % V; }
 
-  __device__ __forceinline__ void load(const T* row, int lane, int D, bool live) {
+  // Values behind the last channel stay as they are: zero from the start.
+  __device__ __forceinline__ void zero() {
 #pragma unroll
     for (int p = 0; p < P; ++p) v[p] = 0;
-    if (!live) return;
+  }
+  __device__ __forceinline__ void load(const T* row, int lane, int D) {
     if constexpr (V == 8) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
@@ -178,7 +180,11 @@ __global__ void __launch_bounds__(threads_of(LANES), MINB) norm_kernel(const Arg
   __shared__ float buf[2][32][2];
   int turn = 0;
   const int lane = threadIdx.x % LANES, sub = threadIdx.x / LANES, h = blockIdx.y, D = a.D;
-  F2 w[P], b[P], sw[BWD ? P : 1], sb[BWD ? P : 1];
+  // w and b of this lane's channels: in registers, or, where the running sums take those (SHARED), in shared memory,
+  // four values of a lane together and the lanes side by side.
+  constexpr bool SHARED = BWD && E >= 16;
+  __shared__ float4 ws[SHARED ? E / 4 : 1][SHARED ? LANES : 1], bs[SHARED ? E / 4 : 1][SHARED ? LANES : 1];
+  F2 wr[SHARED ? 1 : P], br[SHARED ? 1 : P], sw[BWD ? P : 1], sb[BWD ? P : 1];
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     float t[4];
@@ -189,48 +195,63 @@ __global__ void __launch_bounds__(threads_of(LANES), MINB) norm_kernel(const Arg
       t[j] = c < D && a.w ? a.w[at] : 1.f;
       t[2 + j] = c < D && a.b ? a.b[at] : 0.f;
     }
-    w[p] = f2(t[0], t[1]), b[p] = f2(t[2], t[3]);
+    if constexpr (SHARED) {
+      if (sub == 0) {
+        reinterpret_cast<float2*>(&ws[p / 2][lane])[p % 2] = make_float2(t[0], t[1]);
+        reinterpret_cast<float2*>(&bs[p / 2][lane])[p % 2] = make_float2(t[2], t[3]);
+      }
+    } else {
+      wr[p] = f2(t[0], t[1]), br[p] = f2(t[2], t[3]);
+    }
     if constexpr (BWD) sw[p] = sb[p] = f2(0.f);
   }
+  if constexpr (SHARED) __syncthreads();
+  auto w_of = [&](int p) {
+    if constexpr (!SHARED) return wr[p];
+    const float4 v = ws[p / 2][lane];
+    return p % 2 ? f2(v.z, v.w) : f2(v.x, v.y);
+  };
+  auto b_of = [&](int p) {
+    if constexpr (!SHARED) return br[p];
+    const float4 v = bs[p / 2][lane];
+    return p % 2 ? f2(v.z, v.w) : f2(v.x, v.y);
+  };
   // Where this thread's rows lie: of y, z, dy at `row`, of x and dx at `xrow`.  Every thread of the block takes the
   // same number of steps (the barriers of wide rows count on it).
   const long long step = (long long)gridDim.x * ROWS;
+  const size_t row_step = (size_t)step * a.H * D, x_step = a.head_major ? (size_t)step * D : row_step;
   long long tok = (long long)blockIdx.x * ROWS + sub;
   size_t row = ((size_t)tok * a.H + h) * D, xrow = row;
-  uint32_t t = 0;
+  uint32_t t = 0;  // head-major: the token's place in its sequence
   if (a.head_major && tok < a.tokens) {
     const uint32_t bb = a.by_t.quot((uint32_t)tok);
     t = (uint32_t)tok - bb * (uint32_t)a.T;
     xrow = (((size_t)bb * a.H + h) * a.T + t) * D;
   }
-  auto advance = [&]() {
-    tok += step;
-    row += (size_t)step * a.H * D;
-    if (!a.head_major) {
-      xrow = row;
-    } else if (tok < a.tokens) {
+  R nx, nz, nd;
+  nx.zero(), nz.zero(), nd.zero();
+  auto load = [&]() {
+    if (tok >= a.tokens) return;  // what was loaded last stays and is not used
+    nx.load((const T*)a.x + xrow, lane, D);
+    if constexpr (GATE) nz.load((const T*)a.z + row, lane, D);
+    if constexpr (BWD) nd.load((const T*)a.dy + row, lane, D);
+  };
+  load();
+  for (long long first = (long long)blockIdx.x * ROWS; first < a.tokens; first += step) {
+    const R px = nx, pz = nz;
+    R pd = nd;
+    const bool live = tok < a.tokens;
+    if (BWD && !live) pd.zero();  // nothing of it goes into the sums of dw and db
+    const size_t out = row, xout = xrow;
+    tok += step, row += row_step, xrow += x_step;
+    if (a.head_major && tok < a.tokens) {
       t += (uint32_t)step;
-      xrow += (size_t)step * D;
       if (t >= (uint32_t)a.T) {
         const uint32_t q = a.by_t.quot(t);
         t -= q * (uint32_t)a.T;
         xrow += (size_t)q * (a.H - 1) * a.T * D;
       }
     }
-  };
-  R nx, nz, nd;
-  auto load = [&]() {
-    const bool live = tok < a.tokens;
-    nx.load((const T*)a.x + xrow, lane, D, live);
-    if constexpr (GATE) nz.load((const T*)a.z + row, lane, D, live);
-    if constexpr (BWD) nd.load((const T*)a.dy + row, lane, D, live);
-  };
-  load();
-  for (long long first = (long long)blockIdx.x * ROWS; first < a.tokens; first += step) {
-    const R px = nx, pz = nz, pd = nd;
-    const bool live = tok < a.tokens;
-    const size_t out = row, xout = xrow;
-    advance();
     load();  // the next step's row
 
     F2 c[P];  // x less its mean, zero behind the last channel
@@ -253,13 +274,13 @@ __global__ void __launch_bounds__(threads_of(LANES), MINB) norm_kernel(const Arg
     for (int p = 1; p < P; ++p) q2 = fma2(c[p], c[p], q2);
     float q[1] = {lo(q2) + hi(q2)};
     row_sum<LANES>(q, buf, turn);
-    const float rstd = 1.f / sqrtf(q[0] * a.inv_d + a.eps);
+    const float rstd = rsqrtf(q[0] * a.inv_d + a.eps);
     R o;
     if constexpr (!BWD) {
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         F2 slope;
-        const F2 u = fma2(mul2(c[p], f2(rstd)), w[p], b[p]);
+        const F2 u = fma2(mul2(c[p], f2(rstd)), w_of(p), b_of(p));
         o.set(p, GATE ? mul2(u, act2<T, ACT>(pz.get(p), &slope)) : act2<T, ACT>(u, &slope));
       }
       if (live) o.store((T*)a.y + out, lane, D);
@@ -267,7 +288,7 @@ __global__ void __launch_bounds__(threads_of(LANES), MINB) norm_kernel(const Arg
       F2 dn[P], s1 = f2(0.f), s2 = f2(0.f);
 #pragma unroll
       for (int p = 0; p < P; ++p) {
-        const F2 n = mul2(c[p], f2(rstd)), u = fma2(n, w[p], b[p]), d = pd.get(p);
+        const F2 n = mul2(c[p], f2(rstd)), w = w_of(p), u = fma2(n, w, b_of(p)), d = pd.get(p);
         F2 slope, du;
         if constexpr (GATE) {
           du = mul2(d, act2<T, ACT>(pz.get(p), &slope));
@@ -278,7 +299,7 @@ __global__ void __launch_bounds__(threads_of(LANES), MINB) norm_kernel(const Arg
         }
         sw[p] = fma2(du, n, sw[p]);
         sb[p] = add2(sb[p], du);
-        dn[p] = mul2(du, w[p]);
+        dn[p] = mul2(du, w);
         s1 = add2(s1, dn[p]);
         s2 = fma2(dn[p], n, s2);
       }
@@ -324,17 +345,20 @@ __global__ void __launch_bounds__(threads_of(LANES), MINB) norm_kernel(const Arg
 }
 
 // ---------------------------------------------------------------------------------------------------- host
-// Resident blocks that the registers allow: 64 a thread forward at bf16, 80 at fp32, 96 backward (with the sums of dw
-// and db).
+// Threads an SM that the registers allow: 102 registers a thread forward at bf16 (16 values a lane), 85 at fp32 (8),
+// 128 in the backward.  More threads with fewer registers lose more to spills than they hide: the D = 512 case below
+// takes 51 instead of 43 us forward with 768 threads, 126 instead of 77 us backward with 640.
+constexpr int resident(bool bwd, bool wide) { return bwd ? 512 : wide ? 768 : 640; }
 constexpr int blocks_an_sm(int lanes, bool bwd, bool wide) {
-  return (bwd ? 640 : wide ? 768 : 1024) / threads_of(lanes) < 1 ? 1 : (bwd ? 640 : wide ? 768 : 1024) / threads_of(lanes);
+  return resident(bwd, wide) / threads_of(lanes) < 1 ? 1 : resident(bwd, wide) / threads_of(lanes);
 }
 // Blocks a head: enough to fill the 148 SMs of a B200, no more than there are steps, by the lanes that share a row
-// of 8 values a lane.  The same for every alignment and, in the backward, type, so that the workspace follows from the
-// sizes, and for every device, so that the order of the sums does.
+// of 16 values a lane (8 at fp32).  The same for every alignment and, in the backward, which passes wide = false,
+// type, so that the workspace follows from the sizes, and for every device, so that the order of the sums does.
 inline int row_blocks(long long tokens, int H, int D, bool bwd, bool wide) {
-  int lanes = 8;
-  while (lanes * 8 < D) lanes *= 2;
+  const int each = wide ? 8 : 16;
+  int lanes = 64 / each;
+  while (lanes * each < D) lanes *= 2;
   const long long want = (148LL * blocks_an_sm(lanes, bwd, wide) + H - 1) / H;
   const long long most = (tokens + rows_of(lanes) - 1) / rows_of(lanes);
   return (int)(want < most ? want : most);
@@ -358,7 +382,19 @@ int launch(const Args& a, int act, int grid_x, cudaStream_t st) {
 template <typename T, bool BWD>
 int dispatch(const Args& a, int V, int act, int grid_x, cudaStream_t st) {
   const int D = a.D;
-  if (V == 8) {
+  if constexpr (sizeof(T) == 2) {
+    if (V == 8) {
+      if (D <= 64) return launch<T, 8, 4, 2, BWD>(a, act, grid_x, st);
+      if (D <= 128) return launch<T, 8, 8, 2, BWD>(a, act, grid_x, st);
+      if (D <= 256) return launch<T, 8, 16, 2, BWD>(a, act, grid_x, st);
+      if (D <= 512) return launch<T, 8, 32, 2, BWD>(a, act, grid_x, st);
+      if (D <= 1024) return launch<T, 8, 64, 2, BWD>(a, act, grid_x, st);
+      if (D <= 2048) return launch<T, 8, 128, 2, BWD>(a, act, grid_x, st);
+      if (D <= 4096) return launch<T, 8, 256, 2, BWD>(a, act, grid_x, st);
+      if constexpr (BWD) return launch<T, 8, 1024, 1, BWD>(a, act, grid_x, st);
+      else return launch<T, 8, 512, 2, BWD>(a, act, grid_x, st);
+    }
+  } else if (V == 8) {
     if (D <= 64) return launch<T, 8, 8, 1, BWD>(a, act, grid_x, st);
     if (D <= 128) return launch<T, 8, 16, 1, BWD>(a, act, grid_x, st);
     if (D <= 256) return launch<T, 8, 32, 1, BWD>(a, act, grid_x, st);

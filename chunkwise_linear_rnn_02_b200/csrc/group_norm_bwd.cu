@@ -7,8 +7,10 @@ namespace {
 
 // out[c] = sum over r < rows of part[r][c], always in the same order: 32 groups of 32 threads take every 32nd row of
 // 32 columns, and the groups' sums are added one after another.
-__global__ void __launch_bounds__(1024) join_kernel(const float* __restrict__ part_w, const float* __restrict__ part_b,
+__global__ void __launch_bounds__(1024) join_kernel(const float* part_w, const float* part_b,
                                                     float* __restrict__ dw, float* __restrict__ db, int rows, int cols) {
+  // Launched while the kernel before it still runs: nothing is read before that one has ended.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ float s[32][33];
   const float* part = blockIdx.y == 0 ? part_w : part_b;
   float* out = blockIdx.y == 0 ? dw : db;
@@ -17,7 +19,7 @@ __global__ void __launch_bounds__(1024) join_kernel(const float* __restrict__ pa
   float t = 0.f;
   if (c < cols) {
 #pragma unroll 8
-    for (int r = g; r < rows; r += 32) t += __ldg(part + (size_t)r * cols + c);
+    for (int r = g; r < rows; r += 32) t += part[(size_t)r * cols + c];
   }
   s[g][k] = t;
   __syncthreads();
@@ -73,6 +75,16 @@ extern "C" int gla_group_norm_bwd(const void* x, const void* z, const float* w, 
   if (!dw && !db) return GLA_OK;
   // A shared weight row also sums over the heads: the partial rows [grid][H][D] are grid * H rows of D.
   const int rows = weight_rows == 1 ? grid * H : grid, cols = weight_rows * D;
-  join_kernel<<<dim3((cols + 31) / 32, 2), 1024, 0, st>>>(a.part_w, a.part_b, dw, db, rows, cols);
-  return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((cols + 31) / 32, 2);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, join_kernel, (const float*)a.part_w, (const float*)a.part_b, dw, db, rows, cols);
+  if (e != cudaSuccess) (void)cudaGetLastError();
+  return e == cudaSuccess ? GLA_OK : GLA_ERR_CUDA;
 }

@@ -1,16 +1,16 @@
 // Rotary positions of q and k (C ABI in include/gla.h, gla_rotary).
 //
-// The pairs (u, v) of the first R channels of a head turn by A_i = p freq_i; the rest is copied.  HBM-bound:
-// each value is read and written once.  A thread owns one token and one vector of pairs (V pairs in the
-// half layout, V / 2 in the interleaved one), forms their sines and cosines once and applies them to
-// several heads of q and k.  The angle is p freq_i / 2 pi in 64 bits, minus the nearest whole number of
-// turns; the remaining part of a turn is rounded to 32 bits (|r| <= 1/2, off by at most 2^-26 turns), so
-// the angle's error does not grow with the position.
+// The pairs (u, v) of the first R channels of a head turn by A_i = p freq_i; the rest is copied.  HBM-bound: each value
+// is read and written once.  A thread owns one token and two vectors of V channels, forms the sines and cosines of
+// their pairs once and applies them to several heads of q and k, whose vectors it loads four heads at a time.  In the
+// half layout the two vectors are the first and the second halves of V pairs; in the interleaved one they are
+// neighbours.  Copied vectors go the same way without the rotation.
+// The angle is p freq_i / 2 pi in 64 bits, minus the nearest whole number of turns; the remaining part of a turn is
+// rounded to 32 bits (|r| <= 1/2, off by at most 2^-26 turns), so the angle's error does not grow with the position.
 #include <limits.h>
 #include <math.h>
 
 #include "../../include/gla.h"
-#include "fast_path.cuh"
 #include "vec.cuh"
 
 namespace {
@@ -27,18 +27,16 @@ struct Args {
   int pos_rows;
   int Hq, Hk, T, D, R;
   unsigned tokens;  // B * T
-  int items;        // vectors a head: turned ones, then copied ones
+  int items;        // a head's pairs of vectors: turned ones, then copied ones
   int turned;
   int heads_a_thread;
   float scale, sign;
   int in_head_major, out_head_major;
+  int neighbours;  // V = 1: the halves of a pair are channels 2i and 2i + 1
   gla::Divider by_t, by_items;
 };
 
-// Offset of (token (b, t), head h) and the distance between heads.
-__device__ __forceinline__ size_t row_of(bool head_major, uint32_t b, uint32_t t, int h, int H, int T, int D) {
-  return head_major ? (((size_t)b * H + h) * T + t) * D : (((size_t)b * T + t) * H + h) * D;
-}
+constexpr int kBatch = 4;  // heads loaded together
 
 template <typename T, int V, bool INTERLEAVED>
 __global__ void __launch_bounds__(256) rotary_kernel(const Args a) {
@@ -47,92 +45,113 @@ __global__ void __launch_bounds__(256) rotary_kernel(const Args a) {
   if (tok >= a.tokens) return;
   const int item = (int)(idx - tok * (uint32_t)a.items);
   const uint32_t b = a.by_t.quot(tok), t = tok - b * (uint32_t)a.T;
-  const int h0 = blockIdx.y * a.heads_a_thread, h1 = min(h0 + a.heads_a_thread, a.Hq + a.Hk);
 
-  if (item >= a.turned) {  // copied channels
-    const int c = a.R + (item - a.turned) * V;
-    for (int h = h0; h < h1; ++h) {
-      const bool is_q = h < a.Hq;
-      const int hh = is_q ? h : h - a.Hq, H = is_q ? a.Hq : a.Hk;
-      Pack<T, V> p;
-      p.load((const T*)(is_q ? a.q : a.k) + row_of(a.in_head_major, b, t, hh, H, a.T, a.D) + c);
-      p.store((T*)(is_q ? a.qo : a.ko) + row_of(a.out_head_major, b, t, hh, H, a.T, a.D) + c);
+  // The item's two vectors, and which of them turn.
+  int c0, c1;
+  bool turn0, turn1;
+  if constexpr (INTERLEAVED) {
+    c0 = item * 2 * V, c1 = c0 + V;
+    turn0 = c0 < a.R, turn1 = c1 < a.R;
+  } else {
+    turn0 = turn1 = item < a.turned;
+    c0 = turn0 ? (a.neighbours ? 2 * item : item * V) : a.R + (item - a.turned) * 2 * V;
+    c1 = turn0 ? (a.neighbours ? c0 + 1 : c0 + a.R / 2) : c0 + V;
+  }
+  const bool has1 = c1 < a.D;
+
+  float cs[V], sn[V];
+  if (turn0) {
+    long long p = a.pos0;
+    if (a.pos_rows == 0) p += t;
+    else p += a.pos[a.pos_rows == 1 ? (size_t)t : (size_t)tok];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int f = item * V + i;  // the same in both layouts; a second vector that does not turn has none
+      double turns = (double)p * (f < a.R / 2 ? a.freq[f] * 0.15915494309189533577 : 0.0);  // 1 / (2 pi)
+      turns -= rint(turns);
+      sincospif(2.f * (float)turns, &sn[i], &cs[i]);
+      cs[i] *= a.scale;
+      sn[i] *= a.scale * a.sign;
     }
-    return;
   }
-  constexpr int PAIRS = INTERLEAVED ? (V > 1 ? V / 2 : 1) : V;
-  long long p = a.pos0;
-  if (a.pos_rows == 0) p += t;
-  else p += a.pos[a.pos_rows == 1 ? (size_t)t : (size_t)tok];
-  float cs[PAIRS], sn[PAIRS];
+
+  const int h0 = blockIdx.y * a.heads_a_thread, h1 = min(h0 + a.heads_a_thread, a.Hq + a.Hk);
+#pragma unroll 1
+  for (int part = 0; part < 2; ++part) {  // heads of q, then heads of k
+    const int H = part ? a.Hk : a.Hq, first = max(h0 - (part ? a.Hq : 0), 0), last = min(h1 - (part ? a.Hq : 0), H);
+    if (first >= last) continue;
+    const size_t in_stride = a.in_head_major ? (size_t)a.T * a.D : (size_t)a.D;
+    const size_t out_stride = a.out_head_major ? (size_t)a.T * a.D : (size_t)a.D;
+    const T* in = (const T*)(part ? a.k : a.q) +
+                  (a.in_head_major ? ((size_t)b * H * a.T + t) * a.D : (size_t)tok * H * a.D) + first * in_stride;
+    T* out = (T*)(part ? a.ko : a.qo) +
+             (a.out_head_major ? ((size_t)b * H * a.T + t) * a.D : (size_t)tok * H * a.D) + first * out_stride;
+    for (int h = first; h < last; h += kBatch, in += kBatch * in_stride, out += kBatch * out_stride) {
+      Pack<T, V> u[kBatch], v[kBatch];
 #pragma unroll
-  for (int i = 0; i < PAIRS; ++i) {
-    double turns = (double)p * (a.freq[item * PAIRS + i] * 0.15915494309189533577);  // 1 / (2 pi)
-    turns -= rint(turns);
-    sincospif(2.f * (float)turns, &sn[i], &cs[i]);
-    cs[i] *= a.scale;
-    sn[i] *= a.scale * a.sign;
-  }
-  for (int h = h0; h < h1; ++h) {
-    const bool is_q = h < a.Hq;
-    const int hh = is_q ? h : h - a.Hq, H = is_q ? a.Hq : a.Hk;
-    const T* in = (const T*)(is_q ? a.q : a.k) + row_of(a.in_head_major, b, t, hh, H, a.T, a.D);
-    T* out = (T*)(is_q ? a.qo : a.ko) + row_of(a.out_head_major, b, t, hh, H, a.T, a.D);
-    if constexpr (INTERLEAVED) {
-      constexpr int W = V > 1 ? V : 2;  // one pair at a time when nothing wider fits
-      Pack<T, W / (V > 1 ? 1 : 2)> u, v;
-      if constexpr (V > 1) {
-        u.load(in + item * V);
-#pragma unroll
-        for (int i = 0; i < PAIRS; ++i) {
-          const float x = u.get(2 * i), y = u.get(2 * i + 1);
-          u.set(2 * i, x * cs[i] - y * sn[i]);
-          u.set(2 * i + 1, y * cs[i] + x * sn[i]);
+      for (int n = 0; n < kBatch; ++n)
+        if (h + n < last) {
+          u[n].load(in + n * in_stride + c0);
+          if (has1) v[n].load(in + n * in_stride + c1);
         }
-        u.store(out + item * V);
-      } else {
-        u.load(in + item * 2);
-        v.load(in + item * 2 + 1);
-        const float x = u.get(0), y = v.get(0);
-        u.set(0, x * cs[0] - y * sn[0]);
-        v.set(0, y * cs[0] + x * sn[0]);
-        u.store(out + item * 2);
-        v.store(out + item * 2 + 1);
-      }
-    } else {
-      Pack<T, V> u, v;
-      u.load(in + item * V);
-      v.load(in + a.R / 2 + item * V);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float x = u.get(i), y = v.get(i);
-        u.set(i, x * cs[i] - y * sn[i]);
-        v.set(i, y * cs[i] + x * sn[i]);
-      }
-      u.store(out + item * V);
-      v.store(out + a.R / 2 + item * V);
+      for (int n = 0; n < kBatch; ++n)
+        if (h + n < last) {
+          if constexpr (INTERLEAVED) {
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+              if (turn0) {
+                const float x = u[n].get(2 * i), y = u[n].get(2 * i + 1);
+                u[n].set(2 * i, x * cs[i] - y * sn[i]);
+                u[n].set(2 * i + 1, y * cs[i] + x * sn[i]);
+              }
+              if (turn1) {
+                const float x = v[n].get(2 * i), y = v[n].get(2 * i + 1);
+                v[n].set(2 * i, x * cs[V / 2 + i] - y * sn[V / 2 + i]);
+                v[n].set(2 * i + 1, y * cs[V / 2 + i] + x * sn[V / 2 + i]);
+              }
+            }
+          } else if (turn0) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              const float x = u[n].get(i), y = v[n].get(i);
+              u[n].set(i, x * cs[i] - y * sn[i]);
+              v[n].set(i, y * cs[i] + x * sn[i]);
+            }
+          }
+          u[n].store(out + n * out_stride + c0);
+          if (has1) v[n].store(out + n * out_stride + c1);
+        }
     }
   }
 }
 
 template <typename T, int V>
 int launch(Args a, bool interleaved, cudaStream_t st) {
-  a.turned = interleaved ? (V > 1 ? a.R / V : a.R / 2) : a.R / 2 / V;
-  a.items = a.turned + (a.D - a.R) / V;
+  if (interleaved && V > 1) {
+    a.items = (a.D / V + 1) / 2;
+  } else {
+    a.neighbours = interleaved;
+    a.turned = a.R / 2 / V;
+    a.items = a.turned + ((a.D - a.R) / V + 1) / 2;
+  }
   const long long threads = (long long)a.tokens * a.items;
   if (threads > INT_MAX - 256) return GLA_ERR_UNSUPPORTED;
   a.by_items = gla::Divider((uint32_t)a.items);
   // A thread takes several heads, so that its sines serve all of them, as long as enough threads are left.
   const int heads = a.Hq + a.Hk;
-  const long long fill = (long long)gla::fast::sm_count() * 2048;
-  long long per = threads * heads / fill;
-  per = per < 1 ? 1 : per > heads ? heads : per;
-  const long long most_y = 65535;
-  if ((heads + per - 1) / per > most_y) per = (heads + most_y - 1) / most_y;
-  a.heads_a_thread = (int)per;
-  const dim3 grid((unsigned)((threads + 255) / 256), (unsigned)((heads + per - 1) / per));
-  if (interleaved) rotary_kernel<T, V, true><<<grid, 256, 0, st>>>(a);
-  else rotary_kernel<T, V, false><<<grid, 256, 0, st>>>(a);
+  const long long fill = 148LL * 1024;
+  long long groups = (fill + threads - 1) / threads;
+  if (groups > heads) groups = heads;
+  if (groups > 65535) groups = 65535;
+  a.heads_a_thread = (int)((heads + groups - 1) / groups);
+  const dim3 grid((unsigned)((threads + 255) / 256), (unsigned)((heads + a.heads_a_thread - 1) / a.heads_a_thread));
+  if constexpr (V > 1) {
+    if (interleaved) rotary_kernel<T, V, true><<<grid, 256, 0, st>>>(a);
+    else rotary_kernel<T, V, false><<<grid, 256, 0, st>>>(a);
+  } else {
+    rotary_kernel<T, V, false><<<grid, 256, 0, st>>>(a);
+  }
   return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_CUDA;
 }
 
@@ -183,7 +202,7 @@ extern "C" int gla_rotary(const void* q, const void* k, void* qo, void* ko, cons
   while (V > 1) {
     bool fits = piece % V == 0 && D % V == 0;
     for (const void* p : {q, (const void*)qo, a.k, (const void*)a.ko}) fits = fits && gla::aligned_to(p, V * es);
-    if (fits && (!interleaved ? true : V >= 2)) break;
+    if (fits) break;
     V /= 2;
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
