@@ -7,6 +7,7 @@ CUDA tensors, the calls raise instead of computing anything elsewhere.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import re
@@ -353,18 +354,20 @@ def msgla_hold_bwd(dout, s: int):
 
 # ------------------------------------------------------------------------------------------
 # Operators around the recurrences: the elementwise scan, the norm behind them, rotary positions.
+# The calls below are a few microseconds of work for one decoded token, so the checks take the short way first.
 def _operand(name, t, dtype, shape, device):
     """Address of a tensor that has to be a contiguous CUDA tensor of this dtype, shape and device; None stays."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape:
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
+    if not t.is_cuda:
+        raise GLAError("tensors must be CUDA tensors: this library has no CPU path")
+    if t.dtype is not dtype or t.shape != shape:
         raise GLAError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
     if t.device != device:
-        raise GLAError(f"{name} is on {t.device}, the call runs on {device}: tensors must be CUDA tensors of one device"
-                       if device.type == "cuda" else "tensors must be CUDA tensors: this library has no CPU path")
-    if not t.is_contiguous():
-        raise GLAError("tensors must be contiguous")
-    return t.data_ptr()
+        raise GLAError(f"{name} is on {t.device}, the call runs on {device}: tensors must be on one device")
+    raise GLAError("tensors must be contiguous")
 
 
 def _first(t, rank):
@@ -376,16 +379,30 @@ def _first(t, rank):
     return _dtype_code(t), t.device
 
 
+# The current stream's handle without building a Stream object, where this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 def _enqueue(name, device, *args):
     """Call an entry point on the current stream of the tensors' device, which need not be the current one."""
-    fn = getattr(load_library(), name)
-    if torch.cuda.current_device() == device.index:
-        code = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    fn = getattr(_LIB or load_library(), name)
+    i = device.index
+    if torch.cuda.current_device() == i:
+        code = fn(*args, _raw_stream(i))
     else:
-        with torch.cuda.device(device):
-            code = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+        with torch.cuda.device(i):
+            code = fn(*args, _raw_stream(i))
     if code != 0:
         raise GLAError(f"{name}: {status_string(code)}")
+
+
+@functools.lru_cache(maxsize=256)
+def _bytes(query, *sizes):
+    return getattr(load_library(), query)(*sizes)
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
 
 
 SCAN_KEEP = 64  # tokens between the states that scan_fwd(save_states=True) keeps
@@ -404,8 +421,7 @@ def scan_fwd(g, x, h0=None, complement: bool = False, output_final_state: bool =
     o = torch.empty_like(g)
     hT = torch.empty(B, H, D, dtype=torch.float32, device=dev) if output_final_state else None
     hc = torch.empty(B, H, -(-T // SCAN_KEEP), D, dtype=torch.float32, device=dev) if save_states else None
-    _enqueue("gla_scan_fwd", dev, gp, xp, hp, o.data_ptr(), None if hT is None else hT.data_ptr(),
-             None if hc is None else hc.data_ptr(), B, H, T, D, int(complement), dt)
+    _enqueue("gla_scan_fwd", dev, gp, xp, hp, o.data_ptr(), _address(hT), _address(hc), B, H, T, D, complement, dt)
     return o, hT, hc
 
 
@@ -422,10 +438,9 @@ def scan_bwd(g, x, do, h0=None, dhT=None, hc=None, complement: bool = False, nee
     dh0 = torch.empty(B, H, D, dtype=torch.float32, device=dev) if need_dh0 else None
     ws, nb = (None, 0)
     if hc is None:
-        ws, nb = _workspace(load_library().gla_scan_bwd_workspace(B, H, T, D, 0), dev)
-    _enqueue("gla_scan_bwd", dev, gp, xp, hp, hcp, dop, dhp, dg.data_ptr(), dx.data_ptr(),
-             None if dh0 is None else dh0.data_ptr(), B, H, T, D, int(complement), dt,
-             None if ws is None else ws.data_ptr(), nb)
+        ws, nb = _workspace(_bytes("gla_scan_bwd_workspace", B, H, T, D, 0), dev)
+    _enqueue("gla_scan_bwd", dev, gp, xp, hp, hcp, dop, dhp, dg.data_ptr(), dx.data_ptr(), _address(dh0), B, H, T, D,
+             complement, dt, _address(ws), nb)
     return dg, dx, dh0
 
 
@@ -438,7 +453,7 @@ def scan_step(g, x, S, complement: bool = False):
         raise GLAError("scan_step needs the state S")
     Sp = _operand("S", S, torch.float32, g.shape, dev)
     o = torch.empty_like(g)
-    _enqueue("gla_scan_step", dev, gp, xp, Sp, o.data_ptr(), B, H, D, int(complement), dt)
+    _enqueue("gla_scan_step", dev, gp, xp, Sp, o.data_ptr(), B, H, D, complement, dt)
     return o
 
 
@@ -453,20 +468,22 @@ def _choice(name, value, table):
     return table[value]
 
 
-def _norm_args(x, z, w, b, layout):
+def _norm_args(x, z, w, b, kind, act, layout):
+    """Checks; returns dtype code, device, shape of y, weight rows, the pointers, and the codes behind them."""
     dt, dev = _first(x, 4)
-    head_major = _choice("layout", layout, _LAYOUTS) == 0
-    B, H, T, D = x.shape if head_major else (x.shape[0], x.shape[2], x.shape[1], x.shape[3])
+    lay = _choice("layout", layout, _LAYOUTS)
+    B, H, T, D = x.shape
+    if lay:
+        H, T = T, H
     out = (B, T, H, D)
-    rows = H
-    for p in (w, b):
-        if p is not None:
-            rows = p.shape[0] if p.dim() == 2 else -1
-    if rows not in (1, H):
+    p = b if b is not None else w
+    rows = H if p is None else p.shape[0] if p.dim() == 2 else -1
+    if rows != 1 and rows != H:
         raise GLAError(f"w and b must be [H, D] or [1, D] with H = {H}")
-    xp, zp = _operand("x", x, x.dtype, x.shape, dev), _operand("z", z, x.dtype, out, dev)
-    wp, bp = (_operand(n, p, torch.float32, (rows, D), dev) for n, p in (("w", w), ("b", b)))
-    return dt, dev, out, rows, xp, zp, wp, bp
+    f32, wshape = torch.float32, (rows, D)
+    return (dt, dev, out, rows, _operand("x", x, x.dtype, x.shape, dev), _operand("z", z, x.dtype, out, dev),
+            _operand("w", w, f32, wshape, dev), _operand("b", b, f32, wshape, dev),
+            _choice("kind", kind, _NORM_KINDS), _choice("act", act, _ACTS), lay)
 
 
 def group_norm_fwd(x, z=None, w=None, b=None, kind: str = "group", act: str = "silu", eps: float = 1e-5,
@@ -478,28 +495,26 @@ def group_norm_fwd(x, z=None, w=None, b=None, kind: str = "group", act: str = "s
     [B,T,H,D], that is, channels last.  w, b: fp32 [H,D], or [1,D] shared by the heads.  kind: "group" (mean and
     variance) or "rms"; act: "none", "silu", "sigmoid".
     """
-    dt, dev, out, rows, xp, zp, wp, bp = _norm_args(x, z, w, b, layout)
+    dt, dev, out, rows, xp, zp, wp, bp, kind, act, lay = _norm_args(x, z, w, b, kind, act, layout)
     B, T, H, D = out
-    y = torch.empty(out, dtype=x.dtype, device=dev)
-    _enqueue("gla_group_norm_fwd", dev, xp, zp, wp, bp, y.data_ptr(), B, H, T, D, rows,
-             _choice("kind", kind, _NORM_KINDS), _choice("act", act, _ACTS), eps, _LAYOUTS[layout], dt)
+    y = torch.empty(out, dtype=x.dtype, device=dev) if z is None else torch.empty_like(z)
+    _enqueue("gla_group_norm_fwd", dev, xp, zp, wp, bp, y.data_ptr(), B, H, T, D, rows, kind, act, eps, lay, dt)
     return y
 
 
 def group_norm_bwd(x, dy, z=None, w=None, b=None, kind: str = "group", act: str = "silu", eps: float = 1e-5,
                    layout: str = "bhtd"):
     """Backward of group_norm_fwd: returns (dx in x's layout, dz or None, dw or None, db or None)."""
-    dt, dev, out, rows, xp, zp, wp, bp = _norm_args(x, z, w, b, layout)
+    dt, dev, out, rows, xp, zp, wp, bp, kind, act, lay = _norm_args(x, z, w, b, kind, act, layout)
     B, T, H, D = out
-    kind, act = _choice("kind", kind, _NORM_KINDS), _choice("act", act, _ACTS)
     dyp = _operand("dy", dy, x.dtype, out, dev)
     dx = torch.empty_like(x)
     dz = None if z is None else torch.empty_like(z)
-    dw, db = (None if p is None else torch.empty_like(p) for p in (w, b))
-    ws, nb = _workspace(load_library().gla_group_norm_bwd_workspace(B, H, T, D, rows, w is not None, b is not None), dev)
-    _enqueue("gla_group_norm_bwd", dev, xp, zp, wp, bp, dyp, dx.data_ptr(),
-             *(None if t is None else t.data_ptr() for t in (dz, dw, db)), B, H, T, D, rows, kind, act, eps,
-             _LAYOUTS[layout], dt, None if ws is None else ws.data_ptr(), nb)
+    dw = None if w is None else torch.empty_like(w)
+    db = None if b is None else torch.empty_like(b)
+    ws, nb = _workspace(_bytes("gla_group_norm_bwd_workspace", B, H, T, D, rows, w is not None, b is not None), dev)
+    _enqueue("gla_group_norm_bwd", dev, xp, zp, wp, bp, dyp, dx.data_ptr(), _address(dz), _address(dw), _address(db),
+             B, H, T, D, rows, kind, act, eps, lay, dt, _address(ws), nb)
     return dx, dz, dw, db
 
 
@@ -545,26 +560,33 @@ def rotary_frequencies(R: int, base: float = 10000.0, scaling: str = "none", fac
 def _rotary(q, k, freq, pos, pos0, interleaved, scale, inverse, in_layout, out_layout):
     dt, dev = _first(q, 4)
     lin, lout = _choice("layout", in_layout, _LAYOUTS), _choice("out_layout", out_layout, _LAYOUTS)
-    B, D = q.shape[0], q.shape[3]
-    T, Hq = (q.shape[2], q.shape[1]) if lin == 0 else (q.shape[1], q.shape[2])
-    Hk = 0
+    dtype = q.dtype
+    B, Hq, T, D = q.shape
+    if lin:
+        Hq, T = T, Hq
+    qp, kp, Hk, ko = _operand("q", q, dtype, q.shape, dev), None, 0, None
     if k is not None:
         if k.dim() != 4:
             raise GLAError(f"k must have 4 dimensions, got shape {tuple(k.shape)}")
-        Hk = k.shape[1] if lin == 0 else k.shape[2]
-    shape = (lambda H, lay: (B, H, T, D) if lay == 0 else (B, T, H, D))
-    qp, kp = _operand("q", q, q.dtype, shape(Hq, lin), dev), _operand("k", k, q.dtype, shape(Hk, lin), dev)
+        Hk = k.shape[2 if lin else 1]
+        kp = _operand("k", k, dtype, (B, T, Hk, D) if lin else (B, Hk, T, D), dev)
     if freq.dim() != 1:
         raise GLAError(f"freq must be [R/2], got shape {tuple(freq.shape)}")
-    fp = _operand("freq", freq, torch.float64, freq.shape, dev)
-    rows = 0
+    fp, pp, rows = _operand("freq", freq, torch.float64, freq.shape, dev), None, 0
     if pos is not None:
-        rows = 1 if pos.dim() == 1 else B
-    pp = _operand("pos", pos, torch.int64, (T,) if rows == 1 and pos.dim() == 1 else (B, T), dev)
-    qo = torch.empty(shape(Hq, lout), dtype=q.dtype, device=dev)
-    ko = None if k is None else torch.empty(shape(Hk, lout), dtype=q.dtype, device=dev)
-    _enqueue("gla_rotary", dev, qp, kp, qo.data_ptr(), None if ko is None else ko.data_ptr(), fp, pp, int(pos0), rows,
-             B, Hq, Hk, T, D, 2 * freq.shape[0], float(scale), int(interleaved), int(inverse), lin, lout, dt)
+        one = pos.dim() == 1
+        rows = 1 if one else B
+        pp = _operand("pos", pos, torch.int64, (T,) if one else (B, T), dev)
+    if lin == lout:
+        qo = torch.empty_like(q)
+        if k is not None:
+            ko = torch.empty_like(k)
+    else:
+        qo = torch.empty((B, T, Hq, D) if lout else (B, Hq, T, D), dtype=dtype, device=dev)
+        if k is not None:
+            ko = torch.empty((B, T, Hk, D) if lout else (B, Hk, T, D), dtype=dtype, device=dev)
+    _enqueue("gla_rotary", dev, qp, kp, qo.data_ptr(), _address(ko), fp, pp, pos0, rows, B, Hq, Hk, T, D,
+             2 * freq.shape[0], scale, interleaved, inverse, lin, lout, dt)
     return qo, ko
 
 

@@ -2,21 +2,36 @@
 //
 // The pairs (u, v) of the first R channels of a head turn by A_i = p freq_i; the rest is copied.  HBM-bound: each value
 // is read and written once.  A thread owns one token and two vectors of V channels, forms the sines and cosines of
-// their pairs once and applies them to several heads of q and k, whose vectors it loads four heads at a time.  In the
+// their pairs once and applies them to several heads of q and k, whose vectors it loads two heads at a time.  In the
 // half layout the two vectors are the first and the second halves of V pairs; in the interleaved one they are
 // neighbours.  Copied vectors go the same way without the rotation.
-// The angle is p freq_i / 2 pi in 64 bits, minus the nearest whole number of turns; the remaining part of a turn is
-// rounded to 32 bits (|r| <= 1/2, off by at most 2^-26 turns), so the angle's error does not grow with the position.
+// The angle: freq_i / 2 pi, less its whole turns, becomes a 64-bit fraction once a block; its product with the
+// position, whose overflow drops exactly the whole turns, has the angle's part of a turn in its upper word.  (64-bit
+// floating point for every token took most of the kernel's time.)  The word's upper bits, rounded, are the quadrant; the
+// rest, at most 1/8 turn, goes into the Taylor sums of sine and cosine, to x^9 and x^8: what is left out is below
+// (pi/4)^10 / 10! = 2.5e-8.  So the angle's error is that of the fraction, 2^-54 turns, times the position.
+//
+// Measured (bf16): q and k [8, 2048, 4, 256] channels last to head-major 29 us (4.7 TB/s), 39 us with the angles in
+// 64-bit floating point; q, k [1, 8 + 2, 32768, 128], half of it turned, 35 us (4.8 TB/s), 51 us when turned and
+// copied vectors were different threads' work.
 #include <limits.h>
 #include <math.h>
 
 #include "../../include/gla.h"
+#include "pair_math.cuh"
 #include "vec.cuh"
 
 namespace {
 
 using gla::bf16;
+using gla::F2;
+using gla::f2;
+using gla::fma2;
+using gla::hi;
+using gla::lo;
+using gla::mul2;
 using gla::Pack;
+using gla::Two;
 
 struct Args {
   const void *q, *k;
@@ -36,12 +51,34 @@ struct Args {
   gla::Divider by_t, by_items;
 };
 
-constexpr int kBatch = 4;  // heads loaded together
+constexpr int kBatch = 2;  // heads loaded together: four leave registers for half the warps (44 against 29 us)
+
+// Sine and cosine of a 64-bit fraction of a turn.
+__device__ __forceinline__ void sincos_turns(unsigned long long turns, float* sn, float* cs) {
+  const uint32_t w = (uint32_t)(turns >> 32), k = (w + 0x20000000u) >> 30;  // the nearest quadrant
+  const float x = (float)(int)(w - (k << 30)) * 1.4629180792671596e-9f;      // 2 pi / 2^32
+  const float y = x * x;
+  float s = fmaf(y, 1.f / 362880.f, -1.f / 5040.f), c = fmaf(y, 1.f / 40320.f, -1.f / 720.f);
+  s = fmaf(y, s, 1.f / 120.f), c = fmaf(y, c, 1.f / 24.f);
+  s = fmaf(y, s, -1.f / 6.f), c = fmaf(y, c, -0.5f);
+  s = fmaf(x * y, s, x), c = fmaf(y, c, 1.f);
+  const uint32_t p = __float_as_uint(k & 1 ? c : s), q = __float_as_uint(k & 1 ? s : c);
+  *sn = __uint_as_float(p ^ ((k << 30) & 0x80000000u));
+  *cs = __uint_as_float(q ^ (((k + 1) << 30) & 0x80000000u));
+}
 
 template <typename T, int V, bool INTERLEAVED>
-__global__ void __launch_bounds__(256) rotary_kernel(const Args a) {
-  const uint32_t idx = blockIdx.x * 256u + threadIdx.x;
-  const uint32_t tok = a.by_items.quot(idx);
+__global__ void __launch_bounds__(256, 4) rotary_kernel(const Args a) {
+  // The pairs' turns a position as fractions of 2^64.
+  extern __shared__ unsigned long long fraction[];  // [R / 2]
+  for (int f = threadIdx.x; f < a.R / 2; f += 256) {
+    double turns = a.freq[f] * 0.15915494309189533577;  // 1 / (2 pi)
+    turns -= floor(turns);
+    fraction[f] = __double2ull_rn(turns * 18446744073709551616.0);  // 1.0, if it rounds up to that, becomes 2^64 - 1
+  }
+  __syncthreads();
+  const int h0 = blockIdx.y * a.heads_a_thread, h1 = min(h0 + a.heads_a_thread, a.Hq + a.Hk);
+  const uint32_t idx = blockIdx.x * 256u + threadIdx.x, tok = a.by_items.quot(idx);
   if (tok >= a.tokens) return;
   const int item = (int)(idx - tok * (uint32_t)a.items);
   const uint32_t b = a.by_t.quot(tok), t = tok - b * (uint32_t)a.T;
@@ -59,6 +96,8 @@ __global__ void __launch_bounds__(256) rotary_kernel(const Args a) {
   }
   const bool has1 = c1 < a.D;
 
+  // Of the V pairs: in the half layout pair i turns values i of both vectors, in the interleaved one the first V / 2
+  // pairs are those of the first vector.
   float cs[V], sn[V];
   if (turn0) {
     long long p = a.pos0;
@@ -66,16 +105,14 @@ __global__ void __launch_bounds__(256) rotary_kernel(const Args a) {
     else p += a.pos[a.pos_rows == 1 ? (size_t)t : (size_t)tok];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int f = item * V + i;  // the same in both layouts; a second vector that does not turn has none
-      double turns = (double)p * (f < a.R / 2 ? a.freq[f] * 0.15915494309189533577 : 0.0);  // 1 / (2 pi)
-      turns -= rint(turns);
-      sincospif(2.f * (float)turns, &sn[i], &cs[i]);
+      const int f = item * V + i;
+      if (INTERLEAVED && f >= a.R / 2) break;  // of a second vector that does not turn
+      sincos_turns(fraction[f] * (unsigned long long)p, &sn[i], &cs[i]);
       cs[i] *= a.scale;
       sn[i] *= a.scale * a.sign;
     }
   }
 
-  const int h0 = blockIdx.y * a.heads_a_thread, h1 = min(h0 + a.heads_a_thread, a.Hq + a.Hk);
 #pragma unroll 1
   for (int part = 0; part < 2; ++part) {  // heads of q, then heads of k
     const int H = part ? a.Hk : a.Hq, first = max(h0 - (part ? a.Hq : 0), 0), last = min(h1 - (part ? a.Hq : 0), H);
@@ -97,26 +134,28 @@ __global__ void __launch_bounds__(256) rotary_kernel(const Args a) {
 #pragma unroll
       for (int n = 0; n < kBatch; ++n)
         if (h + n < last) {
-          if constexpr (INTERLEAVED) {
+          if constexpr (V == 1) {
+            if (turn0) {
+              const float x = u[n].get(0), y = v[n].get(0);
+              u[n].set(0, x * cs[0] - y * sn[0]);
+              v[n].set(0, y * cs[0] + x * sn[0]);
+            }
+          } else {
+            typedef typename Two<T>::Raw Raw;
+            Raw* ur = reinterpret_cast<Raw*>(u[n].v);
+            Raw* vr = reinterpret_cast<Raw*>(v[n].v);
 #pragma unroll
             for (int i = 0; i < V / 2; ++i) {
-              if (turn0) {
-                const float x = u[n].get(2 * i), y = u[n].get(2 * i + 1);
-                u[n].set(2 * i, x * cs[i] - y * sn[i]);
-                u[n].set(2 * i + 1, y * cs[i] + x * sn[i]);
+              const F2 x = Two<T>::wide(ur[i]), y = Two<T>::wide(vr[i]);
+              if constexpr (INTERLEAVED) {  // (x, y) c + (-y, x) s
+                const F2 xs = f2(-hi(x), lo(x)), ys = f2(-hi(y), lo(y));
+                if (turn0) ur[i] = Two<T>::narrow(fma2(xs, f2(sn[i]), mul2(x, f2(cs[i]))));
+                if (turn1) vr[i] = Two<T>::narrow(fma2(ys, f2(sn[V / 2 + i]), mul2(y, f2(cs[V / 2 + i]))));
+              } else if (turn0) {
+                const F2 c = f2(cs[2 * i], cs[2 * i + 1]), s = f2(sn[2 * i], sn[2 * i + 1]);
+                ur[i] = Two<T>::narrow(fma2(y, f2(-sn[2 * i], -sn[2 * i + 1]), mul2(x, c)));
+                vr[i] = Two<T>::narrow(fma2(x, s, mul2(y, c)));
               }
-              if (turn1) {
-                const float x = v[n].get(2 * i), y = v[n].get(2 * i + 1);
-                v[n].set(2 * i, x * cs[V / 2 + i] - y * sn[V / 2 + i]);
-                v[n].set(2 * i + 1, y * cs[V / 2 + i] + x * sn[V / 2 + i]);
-              }
-            }
-          } else if (turn0) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-              const float x = u[n].get(i), y = v[n].get(i);
-              u[n].set(i, x * cs[i] - y * sn[i]);
-              v[n].set(i, y * cs[i] + x * sn[i]);
             }
           }
           u[n].store(out + n * out_stride + c0);
@@ -146,11 +185,12 @@ int launch(Args a, bool interleaved, cudaStream_t st) {
   if (groups > 65535) groups = 65535;
   a.heads_a_thread = (int)((heads + groups - 1) / groups);
   const dim3 grid((unsigned)((threads + 255) / 256), (unsigned)((heads + a.heads_a_thread - 1) / a.heads_a_thread));
+  const size_t smem = (size_t)(a.R / 2) * sizeof(unsigned long long);  // 32 KB at most
   if constexpr (V > 1) {
-    if (interleaved) rotary_kernel<T, V, true><<<grid, 256, 0, st>>>(a);
-    else rotary_kernel<T, V, false><<<grid, 256, 0, st>>>(a);
+    if (interleaved) rotary_kernel<T, V, true><<<grid, 256, smem, st>>>(a);
+    else rotary_kernel<T, V, false><<<grid, 256, smem, st>>>(a);
   } else {
-    rotary_kernel<T, V, false><<<grid, 256, 0, st>>>(a);
+    rotary_kernel<T, V, false><<<grid, 256, smem, st>>>(a);
   }
   return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_CUDA;
 }
