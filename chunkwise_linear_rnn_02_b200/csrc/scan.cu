@@ -59,14 +59,15 @@ __device__ __forceinline__ F2 shfl2(F2 a, int src) {
 }
 
 // a = exp g and, with REST, 1 - a.  Near g = 0 both come from exp g - 1 = g (1 + g/2 (1 + g/3 (...))), so that
-// neither the 1 - a of a slow gate nor a long product of a's loses its leading digits.  For a alone three terms do up
-// to |g| = 1/32 (what is left out, g^4/24, is below 2^-24); 1 - a takes five terms up to 1/8, where 1 - e^g keeps
-// enough digits.  Elsewhere a state forgets within a few dozen tokens, and the exponential's own error (2^-22 for the
-// approximate one at bf16) has no time to add up.
+// neither the 1 - a of a slow gate nor a long product of a's loses its leading digits.  Five terms do up to |g| = 1/8
+// (what is left out, g^5/720 of it, is below 2^-24), where 1 - e^g keeps enough digits; for a alone at bf16 three terms
+// do up to 1/32 (g^4/24 < 2^-24).  Elsewhere a state forgets within a few tokens (8; 32), and the 2^-22 of the
+// approximate exponential has no time to add up.
 template <typename T, bool REST>
 __device__ __forceinline__ F2 decay(F2 g, F2* rest) {
+  constexpr bool FIVE = REST || sizeof(T) == 4;
   F2 t;
-  if constexpr (REST) {
+  if constexpr (FIVE) {
     t = fma2(g, f2(1.f / 120.f), f2(1.f / 24.f));
     t = fma2(g, t, f2(1.f / 6.f));
   } else {
@@ -75,14 +76,9 @@ __device__ __forceinline__ F2 decay(F2 g, F2* rest) {
   t = fma2(g, t, f2(0.5f));
   t = fma2(g, t, f2(1.f));
   const F2 near = fma2(t, g, f2(1.f));
-  F2 far;
-  if constexpr (sizeof(T) == 2) {
-    const F2 y = mul2(g, f2(gla::fast::kLog2e));
-    far = f2(gla::fast_ex2(lo(y)), gla::fast_ex2(hi(y)));
-  } else {
-    far = f2(expf(lo(g)), expf(hi(g)));
-  }
-  constexpr float kNear = REST ? 0.125f : 0.03125f;
+  const F2 y = mul2(g, f2(gla::fast::kLog2e));
+  const F2 far = f2(gla::fast_ex2(lo(y)), gla::fast_ex2(hi(y)));
+  constexpr float kNear = FIVE ? 0.125f : 0.03125f;
   const bool s0 = fabsf(lo(g)) < kNear, s1 = fabsf(hi(g)) < kNear;
   if constexpr (REST) {
     const F2 rn = mul2(t, mul2(g, f2(-1.f))), rf = fma2(far, f2(-1.f), f2(1.f));
@@ -538,29 +534,50 @@ bool make_map(CUtensorMap* m, const void* base, long long BH, int T, int D, int 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Launches one variant; K blocks of a cluster share a slab.  K is the largest power of two that keeps all blocks
-// running at once, and no more than there are tiles.
+// How a variant with slabs of 2 LPR channels is cut.
+// Forward: blocks of 4 warps, three an SM, 16 tokens a thread; one tile of g is 8 KB (16 KB fp32), so three stages of
+// three blocks fit the 227 KB.  Blocks of 8 warps with the same tile bytes in flight pay for joining twice the warps
+// (B=8, T=2048, C=2048 bf16: 45 against 43 us; B=1, T=32768, C=1024: 72 against 57 us), 8 tokens a thread for twice the
+// joins an element (55 us).  Backward: the third array and the recomputed states take the registers of 8 more tokens:
+// 8 tokens a thread, 8 warps (a tile has to start at a kept state), two blocks an SM; 16 tokens a thread spill (217
+// against 84 us for the complement).
+template <typename T, int LPR, bool BWD>
+struct Shape {
+  static constexpr int W = BWD ? 8 : 4, MINB = BWD ? 2 : 3;
+  static constexpr int R = BWD ? 8 : sizeof(T) == 4 && LPR < 32 ? 8 : 16;
+  static constexpr int STAGES = sizeof(T) == 4 && (BWD || LPR == 32) ? 2 : 3;
+  static constexpr int MAXK = LPR < 32 ? 16 : BWD && sizeof(T) == 4 ? 4 : 8;  // the slots take K LPR 32 bytes
+};
+// K is the largest power of two that keeps all blocks running at once, and no more than there are tiles.
+struct Plan {
+  long long cols;
+  int slabs, tiles, K, places;
+  bool busy() const { return cols * K * 2 > places || K == tiles; }
+};
+template <typename T, int LPR, int LOAD, bool BWD>
+Plan plan(const Args& a, long long BH) {
+  typedef Shape<T, LPR, BWD> S;
+  typedef Block<T, S::W, LPR, S::R, BWD ? 3 : 2, S::STAGES, S::MAXK, true, LOAD> B;
+  Plan p;
+  p.slabs = (a.D + B::CW - 1) / B::CW;
+  p.tiles = (int)(((long long)a.T + B::TILE - 1) / B::TILE);
+  p.cols = BH * p.slabs;
+  p.places = 148 * S::MINB;
+  p.K = 1;
+  while (p.K < S::MAXK && p.K * 2 <= p.tiles && p.cols * p.K * 2 <= p.places) p.K *= 2;
+  return p;
+}
+
 template <typename T, int LPR, int LOAD, bool COMP, bool BWD>
 int launch(Args a, long long BH, cudaStream_t st) {
-  // Forward: blocks of 4 warps, three an SM, 16 tokens a thread; one tile of g is 8 KB (16 KB fp32), so three stages
-  // of three blocks fit the 227 KB.  Blocks of 8 warps with the same tile bytes in flight pay for joining twice the
-  // warps (B=8, T=2048, C=2048 bf16: 45 against 43 us; B=1, T=32768, C=1024: 72 against 57 us), 8 tokens a thread for
-  // twice the joins an element (55 us).  Backward: the third array and the recomputed states take the registers of 8
-  // more tokens: 8 tokens a thread, 8 warps (a tile has to start at a kept state), two blocks an SM; 16 tokens a
-  // thread spill (217 against 84 us for the complement).
-  constexpr int W = BWD ? 8 : 4, MINB = BWD ? 2 : 3;
-  constexpr int R = BWD ? 8 : sizeof(T) == 4 && LPR < 32 ? 8 : 16;
-  constexpr int STAGES = BWD && sizeof(T) == 4 ? 2 : sizeof(T) == 4 && LPR == 32 ? 2 : 3;
-  constexpr int MAXK = LPR < 32 ? 16 : BWD && sizeof(T) == 4 ? 4 : 8;  // likewise: the slots take K LPR 32 bytes
-  constexpr int kFill = 148 * MINB;  // blocks that run at once
+  typedef Shape<T, LPR, BWD> S;
+  constexpr int W = S::W, MINB = S::MINB, R = S::R, STAGES = S::STAGES, MAXK = S::MAXK;
   typedef Block<T, W, LPR, R, BWD ? 3 : 2, STAGES, MAXK, true, LOAD> B;
   constexpr int SMEM = STAGES * B::STAGE;
-  a.slabs = (a.D + B::CW - 1) / B::CW;
-  a.tiles = (int)(((long long)a.T + B::TILE - 1) / B::TILE);
-  const long long cols = BH * a.slabs;
-  int K = 1;
-  while (K < MAXK && K * 2 <= a.tiles && cols * K * 2 <= kFill) K *= 2;
-  a.K = K;
+  const Plan p = plan<T, LPR, LOAD, BWD>(a, BH);
+  const int K = p.K;
+  const long long cols = p.cols;
+  a.slabs = p.slabs, a.tiles = p.tiles, a.K = K;
   a.steps = (a.tiles + K - 1) / K;
   Maps maps;
   if (LOAD == kTma && a.T > 0)
@@ -603,13 +620,13 @@ int launch(Args a, long long BH, cudaStream_t st) {
   return GLA_OK;
 }
 
-// Slabs of 64 channels make rows of 128 bytes or more; where even clusters of them leave most SMs idle, slabs of 16
-// channels, in tiles of 256 tokens and clusters of up to 16, give more blocks.
+// Slabs of 64 channels make rows of 128 bytes or more; where even clusters of them leave half of the places for blocks
+// empty, slabs of 32 and then of 16 channels, in longer tiles and larger clusters, give more blocks.
 template <typename T, int LOAD, bool COMP, bool BWD>
 int choose(const Args& a, long long BH, cudaStream_t st) {
-  const long long wide = BH * ((a.D + 63) / 64), tiles = ((long long)a.T + 63) / 64;
-  if (wide * (tiles < 8 ? tiles : 8) * 2 <= 296 && tiles > 8) return launch<T, 8, LOAD, COMP, BWD>(a, BH, st);
-  return launch<T, 32, LOAD, COMP, BWD>(a, BH, st);
+  if (plan<T, 32, LOAD, BWD>(a, BH).busy()) return launch<T, 32, LOAD, COMP, BWD>(a, BH, st);
+  if (plan<T, 16, LOAD, BWD>(a, BH).busy()) return launch<T, 16, LOAD, COMP, BWD>(a, BH, st);
+  return launch<T, 8, LOAD, COMP, BWD>(a, BH, st);
 }
 
 template <bool BWD>
