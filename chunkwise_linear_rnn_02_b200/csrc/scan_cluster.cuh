@@ -7,7 +7,7 @@
 namespace gla {
 namespace cluster {
 
-// BYTES (4, 8 or 16) from global to shared memory; zeros when `in` is false (src is then not read).
+// BYTES (4 or 8) from global to shared memory; zeros when `in` is false (src is then not read).
 template <int BYTES>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool in) {
   const int n = in ? BYTES : 0;
