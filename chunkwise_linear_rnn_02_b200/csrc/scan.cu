@@ -8,7 +8,7 @@
 // pairs are joined in token order across the lanes of a warp (shuffles), the warps of a block (shared memory) and the
 // blocks of a cluster (their shared memory), and then each thread walks its run again from the state that enters it.
 //
-// Split: a block owns a slab of 2 LPR channels and steps through the tokens; a step is a tile of 8 (32 / LPR) R
+// Split: a block owns a slab of 2 LPR channels and steps through the tokens; a step is a tile of 4 (32 / LPR) R
 // tokens.  Where there are too few slabs to fill the SMs, K blocks of a cluster share a slab and take its tiles in
 // turn.  Each step every block sends its (A, H) to all blocks of the cluster (st.async onto an mbarrier in the
 // receiver's shared memory); every block folds all K of them, in token order, into a carry of its own.  So nothing
@@ -544,21 +544,27 @@ bool make_map(CUtensorMap* m, const void* base, long long BH, int T, int D, int 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// How a variant with slabs of 2 LPR channels is cut.
-// Forward: blocks of 4 warps, three an SM, 16 tokens a thread; one tile of g is 8 KB (16 KB fp32), so three stages of
-// three blocks fit the 227 KB.  Blocks of 8 warps with the same tile bytes in flight pay for joining twice the warps
-// (B=8, T=2048, C=2048 bf16: 45 against 43 us; B=1, T=32768, C=1024: 72 against 57 us), 8 tokens a thread for twice the
-// joins an element (55 us).  Backward: the third array and the recomputed states take the registers of 8 more tokens:
-// 8 tokens a thread, 8 warps (a tile has to start at a kept state), two blocks an SM; 16 tokens a thread spill (217
-// against 84 us for the complement).
+// How a variant with slabs of 2 LPR channels is cut: blocks of W warps, MINB of them an SM, R tokens a thread, STAGES
+// tiles in shared memory, up to MAXK blocks a cluster.
+// Blocks of 4 warps: 8 warps with the same bytes in flight pay for joining twice the warps (B=8, T=2048, C=2048 bf16
+// forward 45 against 43 us; B=1, T=32768, C=1024: 72 against 57 us).  Forward: 16 tokens a thread, since 8 make twice
+// the joins an element (55 us); one tile of g is 8 KB (16 KB fp32), so three stages of three blocks fit the 227 KB.
+// Backward: the third array and the recomputed states take the registers of the other 8 tokens (with 16, spills: 217
+// against 84 us for the complement), and a tile has to start at a kept state, so slabs of 64 channels would need 8
+// warps: slabs of 32 are its widest (B=8, T=2048, C=2048 bf16 63 against 65 us; fp32 3 x 2 x 1531 x 333: 18 against 21).
+// The exchange takes longer the more blocks share a slab, so wide slabs leave the larger clusters to the narrower ones
+// (fp32 3 x 2 x 1531 x 333 forward: 17 us with K = 8 and slabs of 64, 13 us with K = 4 and slabs of 32; B=1, T=32768,
+// C=1024 bf16 backward: 108 us with K = 8 and slabs of 32, 92 us with K = 6 and slabs of 16).
 template <typename T, int LPR, bool BWD>
 struct Shape {
-  static constexpr int W = BWD ? 8 : 4, MINB = BWD ? 2 : 3;
-  static constexpr int R = BWD ? 8 : sizeof(T) == 4 && LPR < 32 ? 8 : 16;
-  static constexpr int STAGES = sizeof(T) == 4 && (BWD || LPR == 32) ? 2 : 3;
-  static constexpr int MAXK = LPR < 32 ? 16 : BWD && sizeof(T) == 4 ? 4 : 8;  // the slots take K LPR 32 bytes
+  static_assert(!BWD || LPR < 32, "a tile of the backward starts at a kept state");
+  static constexpr int W = 4, MINB = BWD && LPR == 16 && sizeof(T) == 2 ? 4 : 3;
+  static constexpr int R = BWD || (sizeof(T) == 4 && LPR < 32) ? 8 : 16;
+  static constexpr int STAGES = sizeof(T) == 4 && LPR == 32 ? 2 : 3;
+  static constexpr int MAXK = LPR == 8 ? 16 : LPR == 16 && !BWD ? 8 : 6;
 };
-// K is the largest power of two that keeps all blocks running at once, and no more than there are tiles.
+// K is the largest of 2, 3, 4, 6, 8, 16 that keeps all blocks running at once, and no more than there are tiles.  (In
+// between, clusters leave places free: B=1, T=32768, C=1024 forward 65 us with 13 blocks, 47 us with 8.)
 struct Plan {
   long long cols;
   int slabs, tiles, K, places;
@@ -574,7 +580,8 @@ Plan plan(const Args& a, long long BH) {
   p.cols = BH * p.slabs;
   p.places = 148 * S::MINB;
   p.K = 1;
-  while (p.K < S::MAXK && p.K * 2 <= p.tiles && p.cols * p.K * 2 <= p.places) p.K *= 2;
+  for (int K : {2, 3, 4, 6, 8, 16})
+    if (K <= S::MAXK && K <= p.tiles && p.cols * K <= p.places) p.K = K;
   return p;
 }
 
@@ -630,11 +637,12 @@ int launch(Args a, long long BH, cudaStream_t st) {
   return GLA_OK;
 }
 
-// Slabs of 64 channels make rows of 128 bytes or more; where even clusters of them leave half of the places for blocks
-// empty, slabs of 32 and then of 16 channels, in longer tiles and larger clusters, give more blocks.
+// Slabs of 64 channels (32 in the backward) make the longest rows; where even clusters of them leave half of the places
+// for blocks empty, slabs of 32 and then of 16 channels, in longer tiles and larger clusters, give more blocks.
 template <typename T, int LOAD, bool COMP, bool BWD>
 int choose(const Args& a, long long BH, cudaStream_t st) {
-  if (plan<T, 32, LOAD, BWD>(a, BH).busy()) return launch<T, 32, LOAD, COMP, BWD>(a, BH, st);
+  if constexpr (!BWD)
+    if (plan<T, 32, LOAD, BWD>(a, BH).busy()) return launch<T, 32, LOAD, COMP, BWD>(a, BH, st);
   if (plan<T, 16, LOAD, BWD>(a, BH).busy()) return launch<T, 16, LOAD, COMP, BWD>(a, BH, st);
   return launch<T, 8, LOAD, COMP, BWD>(a, BH, st);
 }
