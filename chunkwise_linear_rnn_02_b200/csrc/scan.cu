@@ -552,46 +552,57 @@ bool make_map(CUtensorMap* m, const void* base, long long BH, int T, int D, int 
 // Backward: the third array and the recomputed states take the registers of the other 8 tokens (with 16, spills: 217
 // against 84 us for the complement), and a tile has to start at a kept state, so slabs of 64 channels would need 8
 // warps: slabs of 32 are its widest (B=8, T=2048, C=2048 bf16 63 against 65 us; fp32 3 x 2 x 1531 x 333: 18 against 21).
-// The exchange takes longer the more blocks share a slab, so wide slabs leave the larger clusters to the narrower ones
-// (fp32 3 x 2 x 1531 x 333 forward: 17 us with K = 8 and slabs of 64, 13 us with K = 4 and slabs of 32; B=1, T=32768,
-// C=1024 bf16 backward: 108 us with K = 8 and slabs of 32, 92 us with K = 6 and slabs of 16).
 template <typename T, int LPR, bool BWD>
 struct Shape {
   static_assert(!BWD || LPR < 32, "a tile of the backward starts at a kept state");
   static constexpr int W = 4, MINB = BWD && LPR == 16 && sizeof(T) == 2 ? 4 : 3;
   static constexpr int R = BWD || (sizeof(T) == 4 && LPR < 32) ? 8 : 16;
   static constexpr int STAGES = sizeof(T) == 4 && LPR == 32 ? 2 : 3;
-  static constexpr int MAXK = LPR == 8 ? 16 : LPR == 16 && !BWD ? 8 : 6;
+  static constexpr int MAXK = LPR == 8 ? 16 : LPR == 16 ? 8 : 6;
 };
-// K is the largest of 2, 3, 4, 6, 8, 16 that keeps all blocks running at once, and no more than there are tiles.  (In
-// between, clusters leave places free: B=1, T=32768, C=1024 forward 65 us with 13 blocks, 47 us with 8.)
+
+// How many blocks share a slab, and what that costs.  A step of a block takes a fixed time, more the more blocks
+// exchange, and the work of a tile times the blocks of the SM, somewhat more for narrower rows (their lanes also join
+// across the warp):
+//     cost = steps (0.3 + 0.08 K + 0.6 (R / 16) blocks_an_sm share)
+// fitted to 34 shapes (both types and directions, 256 to 65,536 tokens, 64 to 16,384 channels in all, every K and
+// slab): what it chooses takes 1.04 times as long as the best choice on average.  K is 1, 2, 3, 4, 6, 8 or 16, all
+// blocks running at once (in between, clusters leave places free: B=1, T=32768, C=1024 forward 65 us with 13, 47 us
+// with 8), and clusters of six and more take seven eighths of the places at most, since how they fill the GPU's groups
+// of SMs differs from one GPU to the next (2 x 2 x 3000 x 200 bf16 backward: 16 us with 52 clusters of 8, 13 us with 52 of 6;
+// fp32 3 x 2 x 1531 x 333 forward with 66 of 6: 13 us on one GPU, 18 us on another).
 struct Plan {
-  long long cols;
-  int slabs, tiles, K, places;
-  bool busy() const { return cols * K * 2 > places || K == tiles; }
+  long long cols = 0;
+  int slabs = 0, tiles = 0, K = 0;
+  double cost = 0.;
 };
 template <typename T, int LPR, int LOAD, bool BWD>
 Plan plan(const Args& a, long long BH) {
   typedef Shape<T, LPR, BWD> S;
   typedef Block<T, S::W, LPR, S::R, BWD ? 3 : 2, S::STAGES, S::MAXK, true, LOAD> B;
-  Plan p;
-  p.slabs = (a.D + B::CW - 1) / B::CW;
-  p.tiles = (int)(((long long)a.T + B::TILE - 1) / B::TILE);
-  p.cols = BH * p.slabs;
-  p.places = 148 * S::MINB;
-  p.K = 1;
-  for (int K : {2, 3, 4, 6, 8, 16})
-    if (K <= S::MAXK && K <= p.tiles && p.cols * K <= p.places) p.K = K;
-  return p;
+  constexpr int SHARED = S::STAGES * B::STAGE + S::W * LPR * (BWD ? 48 : 32) + (int)sizeof(typename B::Ex) + 1088;
+  constexpr int PLACES = 148 * (S::MINB < 233472 / SHARED ? S::MINB : 233472 / SHARED);  // 228 KB an SM
+  constexpr double share = LPR == 8 ? 1.5 : LPR == 16 && !BWD ? 1.2 : 1.0;
+  Plan best;
+  best.slabs = (a.D + B::CW - 1) / B::CW;
+  best.tiles = (int)(((long long)a.T + B::TILE - 1) / B::TILE);
+  best.cols = BH * best.slabs;
+  for (int K : {1, 2, 3, 4, 6, 8, 16}) {
+    const long long n = best.cols * K;
+    if (K > 1 && (K > S::MAXK || K > best.tiles || n > (K < 6 ? PLACES : PLACES / 8 * 7))) break;
+    const double c = (double)((best.tiles + K - 1) / K) *
+                     (0.3 + (K > 1 ? 0.08 * K : 0.) + 0.6 * S::R / 16 * (double)((n + 147) / 148) * share);
+    if (K == 1 || c < best.cost) best.K = K, best.cost = c;
+  }
+  return best;
 }
 
 template <typename T, int LPR, int LOAD, bool COMP, bool BWD>
-int launch(Args a, long long BH, cudaStream_t st) {
+int launch(Args a, const Plan& p, long long BH, cudaStream_t st) {
   typedef Shape<T, LPR, BWD> S;
   constexpr int W = S::W, MINB = S::MINB, R = S::R, STAGES = S::STAGES, MAXK = S::MAXK;
   typedef Block<T, W, LPR, R, BWD ? 3 : 2, STAGES, MAXK, true, LOAD> B;
   constexpr int SMEM = STAGES * B::STAGE;
-  const Plan p = plan<T, LPR, LOAD, BWD>(a, BH);
   const int K = p.K;
   const long long cols = p.cols;
   a.slabs = p.slabs, a.tiles = p.tiles, a.K = K;
@@ -637,14 +648,16 @@ int launch(Args a, long long BH, cudaStream_t st) {
   return GLA_OK;
 }
 
-// Slabs of 64 channels (32 in the backward) make the longest rows; where even clusters of them leave half of the places
-// for blocks empty, slabs of 32 and then of 16 channels, in longer tiles and larger clusters, give more blocks.
+// Slabs of 64 (forward), 32 or 16 channels, whichever costs least.
 template <typename T, int LOAD, bool COMP, bool BWD>
 int choose(const Args& a, long long BH, cudaStream_t st) {
-  if constexpr (!BWD)
-    if (plan<T, 32, LOAD, BWD>(a, BH).busy()) return launch<T, 32, LOAD, COMP, BWD>(a, BH, st);
-  if (plan<T, 16, LOAD, BWD>(a, BH).busy()) return launch<T, 16, LOAD, COMP, BWD>(a, BH, st);
-  return launch<T, 8, LOAD, COMP, BWD>(a, BH, st);
+  const Plan mid = plan<T, 16, LOAD, BWD>(a, BH), narrow = plan<T, 8, LOAD, BWD>(a, BH);
+  if constexpr (!BWD) {
+    const Plan wide = plan<T, 32, LOAD, BWD>(a, BH);
+    if (wide.cost <= mid.cost && wide.cost <= narrow.cost) return launch<T, 32, LOAD, COMP, BWD>(a, wide, BH, st);
+  }
+  if (mid.cost <= narrow.cost) return launch<T, 16, LOAD, COMP, BWD>(a, mid, BH, st);
+  return launch<T, 8, LOAD, COMP, BWD>(a, narrow, BH, st);
 }
 
 template <bool BWD>
