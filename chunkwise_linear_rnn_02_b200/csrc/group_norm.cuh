@@ -44,25 +44,21 @@ struct Args {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// 1 / (1 + e^-v).  bf16 results carry 8 bits: the approximate exponential and reciprocal (2^-22) do for them.
-template <typename T>
+// 1 / (1 + e^-v) by the approximate exponential and reciprocal: off by 2^-22 or so of itself, and by |v| 2^-24 more where
+// it is small for a far v.  (fp32 gates through the exact ones cost a quarter of the forward's time.)
 __device__ __forceinline__ F2 sigmoid2(F2 v) {
-  if constexpr (sizeof(T) == 2) {
-    const F2 y = mul2(v, f2(-kLog2e));
-    const F2 q = add2(f2(fast_ex2(lo(y)), fast_ex2(hi(y))), f2(1.f));
-    return f2(fast_rcp(lo(q)), fast_rcp(hi(q)));
-  } else {
-    return f2(1.f / (1.f + expf(-lo(v))), 1.f / (1.f + expf(-hi(v))));
-  }
+  const F2 y = mul2(v, f2(-kLog2e));
+  const F2 q = add2(f2(fast_ex2(lo(y)), fast_ex2(hi(y))), f2(1.f));
+  return f2(fast_rcp(lo(q)), fast_rcp(hi(q)));
 }
 // act(v) and its derivative.
-template <typename T, int ACT>
+template <int ACT>
 __device__ __forceinline__ F2 act2(F2 v, F2* slope) {
   if constexpr (ACT == GLA_ACT_NONE) {
     *slope = f2(1.f);
     return v;
   } else {
-    const F2 s = sigmoid2<T>(v), rest = fma2(s, f2(-1.f), f2(1.f));
+    const F2 s = sigmoid2(v), rest = fma2(s, f2(-1.f), f2(1.f));
     if constexpr (ACT == GLA_ACT_SIGMOID) {
       *slope = mul2(s, rest);
       return s;
@@ -100,8 +96,8 @@ __device__ __forceinline__ void row_sum(float (&s)[N], float (*buf)[32][2], int&
 }
 
 // A lane's values of a row: NV vectors of V neighbouring channels, vector i of lane l being number l + i LANES, kept
-// as pairs of values.  V is 8, or 2 or 1 where rows or tensors are not aligned to more; a pair is two values of a
-// vector, or of two vectors where V is 1.
+// as pairs of values.  A vector is 16 bytes, or 2 values or 1 where rows or tensors are not aligned to more; a pair is
+// two values of a vector, or of two vectors where V is 1.
 template <typename T, int V, int LANES, int NV>
 struct Row {
   static constexpr int E = V * NV, P = E / 2;
@@ -116,15 +112,11 @@ struct Row {
     for (int p = 0; p < P; ++p) v[p] = 0;
   }
   __device__ __forceinline__ void load(const T* row, int lane, int D) {
-    if constexpr (V == 8) {
+    if constexpr (V * sizeof(T) == 16) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (channel(lane, i * V) < D) {
-          const uint4* src = reinterpret_cast<const uint4*>(row + channel(lane, i * V));
-          uint4* dst = reinterpret_cast<uint4*>(v + i * (V / 2));
-#pragma unroll
-          for (int k = 0; k < (int)sizeof(T) / 2; ++k) dst[k] = __ldg(src + k);
-        }
+        if (channel(lane, i * V) < D)
+          reinterpret_cast<uint4*>(v)[i] = __ldg(reinterpret_cast<const uint4*>(row + channel(lane, i * V)));
     } else if constexpr (V == 2) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
@@ -142,15 +134,11 @@ struct Row {
     }
   }
   __device__ __forceinline__ void store(T* row, int lane, int D) const {
-    if constexpr (V == 8) {
+    if constexpr (V * sizeof(T) == 16) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (channel(lane, i * V) < D) {
-          uint4* dst = reinterpret_cast<uint4*>(row + channel(lane, i * V));
-          const uint4* src = reinterpret_cast<const uint4*>(v + i * (V / 2));
-#pragma unroll
-          for (int k = 0; k < (int)sizeof(T) / 2; ++k) dst[k] = src[k];
-        }
+        if (channel(lane, i * V) < D)
+          *reinterpret_cast<uint4*>(row + channel(lane, i * V)) = reinterpret_cast<const uint4*>(v)[i];
     } else if constexpr (V == 2) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
@@ -182,7 +170,7 @@ __global__ void __launch_bounds__(threads_of(LANES), MINB) norm_kernel(const Arg
   const int lane = threadIdx.x % LANES, sub = threadIdx.x / LANES, h = blockIdx.y, D = a.D;
   // w and b of this lane's channels: in registers, or, where the running sums take those (SHARED), in shared memory,
   // four values of a lane together and the lanes side by side.
-  constexpr bool SHARED = BWD && E >= 16;
+  constexpr bool SHARED = BWD && E >= 8 && LANES * E <= 4096;  // 32 KB at most
   __shared__ float4 ws[SHARED ? E / 4 : 1][SHARED ? LANES : 1], bs[SHARED ? E / 4 : 1][SHARED ? LANES : 1];
   F2 wr[SHARED ? 1 : P], br[SHARED ? 1 : P], sw[BWD ? P : 1], sb[BWD ? P : 1];
 #pragma unroll
@@ -281,7 +269,7 @@ __global__ void __launch_bounds__(threads_of(LANES), MINB) norm_kernel(const Arg
       for (int p = 0; p < P; ++p) {
         F2 slope;
         const F2 u = fma2(mul2(c[p], f2(rstd)), w_of(p), b_of(p));
-        o.set(p, GATE ? mul2(u, act2<T, ACT>(pz.get(p), &slope)) : act2<T, ACT>(u, &slope));
+        o.set(p, GATE ? mul2(u, act2<ACT>(pz.get(p), &slope)) : act2<ACT>(u, &slope));
       }
       if (live) o.store((T*)a.y + out, lane, D);
     } else {
@@ -291,10 +279,10 @@ __global__ void __launch_bounds__(threads_of(LANES), MINB) norm_kernel(const Arg
         const F2 n = mul2(c[p], f2(rstd)), w = w_of(p), u = fma2(n, w, b_of(p)), d = pd.get(p);
         F2 slope, du;
         if constexpr (GATE) {
-          du = mul2(d, act2<T, ACT>(pz.get(p), &slope));
+          du = mul2(d, act2<ACT>(pz.get(p), &slope));
           o.set(p, mul2(mul2(d, u), slope));
         } else {
-          act2<T, ACT>(u, &slope);
+          act2<ACT>(u, &slope);
           du = mul2(d, slope);
         }
         sw[p] = fma2(du, n, sw[p]);
@@ -345,12 +333,13 @@ __global__ void __launch_bounds__(threads_of(LANES), MINB) norm_kernel(const Arg
 }
 
 // ---------------------------------------------------------------------------------------------------- host
-// Threads an SM that the registers allow: 102 registers a thread forward at bf16 (16 values a lane), 85 at fp32 (8),
-// 128 in the backward.  More threads with fewer registers lose more to spills than they hide: the D = 512 case below
-// takes 51 instead of 43 us forward with 768 threads, 126 instead of 77 us backward with 640.
-constexpr int resident(bool bwd, bool wide) { return bwd ? 512 : wide ? 768 : 640; }
+// Threads an SM that the registers allow: 102 to 128 registers a thread at bf16 (16 values a lane), 85 at fp32 (8), 128
+// in the backward.  More threads with fewer registers lose more to spills than they hide: the D = 512 case above takes 45
+// instead of 36 us forward with 768 threads; short rows, which shuffle less, want the registers (H=8, D=64: 8.6 us with
+// 512 threads, 11.6 us with 640).
+constexpr int resident(int lanes, bool bwd, bool wide) { return bwd ? 512 : wide ? 768 : lanes <= 16 ? 512 : 640; }
 constexpr int blocks_an_sm(int lanes, bool bwd, bool wide) {
-  return resident(bwd, wide) / threads_of(lanes) < 1 ? 1 : resident(bwd, wide) / threads_of(lanes);
+  return resident(lanes, bwd, wide) / threads_of(lanes) < 1 ? 1 : resident(lanes, bwd, wide) / threads_of(lanes);
 }
 // Blocks a head: enough to fill the 148 SMs of a B200, no more than there are steps, by the lanes that share a row
 // of 16 values a lane (8 at fp32).  The same for every alignment and, in the backward, which passes wide = false,
@@ -394,15 +383,17 @@ int dispatch(const Args& a, int V, int act, int grid_x, cudaStream_t st) {
       if constexpr (BWD) return launch<T, 8, 1024, 1, BWD>(a, act, grid_x, st);
       else return launch<T, 8, 512, 2, BWD>(a, act, grid_x, st);
     }
-  } else if (V == 8) {
-    if (D <= 64) return launch<T, 8, 8, 1, BWD>(a, act, grid_x, st);
-    if (D <= 128) return launch<T, 8, 16, 1, BWD>(a, act, grid_x, st);
-    if (D <= 256) return launch<T, 8, 32, 1, BWD>(a, act, grid_x, st);
-    if (D <= 512) return launch<T, 8, 64, 1, BWD>(a, act, grid_x, st);
-    if (D <= 1024) return launch<T, 8, 128, 1, BWD>(a, act, grid_x, st);
-    if (D <= 2048) return launch<T, 8, 256, 1, BWD>(a, act, grid_x, st);
-    if (D <= 4096) return launch<T, 8, 512, 1, BWD>(a, act, grid_x, st);
-    return launch<T, 8, 1024, 1, BWD>(a, act, grid_x, st);
+  } else if constexpr (sizeof(T) == 4) {
+    if (V == 4) {
+      if (D <= 64) return launch<T, 4, 8, 2, BWD>(a, act, grid_x, st);
+      if (D <= 128) return launch<T, 4, 16, 2, BWD>(a, act, grid_x, st);
+      if (D <= 256) return launch<T, 4, 32, 2, BWD>(a, act, grid_x, st);
+      if (D <= 512) return launch<T, 4, 64, 2, BWD>(a, act, grid_x, st);
+      if (D <= 1024) return launch<T, 4, 128, 2, BWD>(a, act, grid_x, st);
+      if (D <= 2048) return launch<T, 4, 256, 2, BWD>(a, act, grid_x, st);
+      if (D <= 4096) return launch<T, 4, 512, 2, BWD>(a, act, grid_x, st);
+      return launch<T, 4, 1024, 2, BWD>(a, act, grid_x, st);
+    }
   }
   if (V == 2) {
     if (D <= 64) return launch<T, 2, 32, 1, BWD>(a, act, grid_x, st);
@@ -443,7 +434,7 @@ inline int check_kind(int kind, int act, float eps, int layout, int dtype) {
   return GLA_OK;
 }
 
-// The vector length: 8 where rows and every tensor start on 16 bytes, else 2 or 1 values.
+// The vector length: 16 bytes where rows and every tensor start on them, else 2 or 1 values.
 inline int vector_of(const Args& a, size_t es) {
   auto fits = [&](int v, size_t bytes) {
     if (a.D % v != 0 || a.D * es % bytes != 0) return false;
@@ -451,7 +442,8 @@ inline int vector_of(const Args& a, size_t es) {
       if (!aligned_to(p, bytes)) return false;
     return true;
   };
-  return fits(8, 16) ? 8 : fits(2, 2 * es) ? 2 : 1;
+  const int wide = (int)(16 / es);
+  return fits(wide, 16) ? wide : fits(2, 2 * es) ? 2 : 1;
 }
 
 inline Args make_args(const void* x, const void* z, const float* w, const float* b, int B, int H, int T, int D,
