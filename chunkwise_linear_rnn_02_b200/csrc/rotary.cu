@@ -11,9 +11,10 @@
 // rest, at most 1/8 turn, goes into the Taylor sums of sine and cosine, to x^9 and x^8: what is left out is below
 // (pi/4)^10 / 10! = 2.5e-8.  So the angle's error is that of the fraction, 2^-54 turns, times the position.
 //
-// Measured (bf16): q and k [8, 2048, 4, 256] channels last to head-major 29 us (4.7 TB/s), 39 us with the angles in
-// 64-bit floating point; q, k [1, 8 + 2, 32768, 128], half of it turned, 35 us (4.8 TB/s), 51 us when turned and
-// copied vectors were different threads' work.
+// Measured (bf16, replays of a CUDA graph of 20 calls): q and k [8, 2048, 4, 256] channels last to head-major 23 us
+// (5.9 TB/s), half as long again with the angles in 64-bit floating point; q, k [1, 8 + 2, 32768, 128], half of it turned,
+// 31 us (5.5 TB/s), two fifths longer when turned and copied vectors were different threads' work; 16 x (8 + 8) x 128,
+// one token, 2.6 us.
 #include <limits.h>
 #include <math.h>
 
@@ -51,7 +52,7 @@ struct Args {
   gla::Divider by_t, by_items;
 };
 
-constexpr int kBatch = 2;  // heads loaded together: four leave registers for half the warps (44 against 29 us)
+constexpr int kBatch = 2;  // heads loaded together: four leave registers for half the warps and take half as long again
 
 // Sine and cosine of a 64-bit fraction of a turn.
 __device__ __forceinline__ void sincos_turns(unsigned long long turns, float* sn, float* cs) {

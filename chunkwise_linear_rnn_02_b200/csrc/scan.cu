@@ -2,6 +2,10 @@
 //
 //     h_t = a_t h_{t-1} + b_t,   a_t = exp g_t,   b_t = x_t  or  (1 - a_t) x_t
 //
+// Measured, bf16: B=8, T=2048, C=2048 forward 34 us (5.9 TB/s), backward 62 us (5.4 TB/s), for the complement 39 and
+// 80 us; B=1, T=32768, C=1024 (clusters of eight and six) forward 47 us, backward 91 us; one token of 32 x 2048 1.5 us.
+// fp32, B=8, T=2048, C=2048: 65 us (6.1 TB/s) and 110 us (6.1 TB/s).
+//
 // HBM-bound: g and x are read once and o written once.  A run of tokens acts on the state in front of it as
 // h -> A h + H with A the product of its a's and H its end state from zero, and two runs one after the other
 // act as (A2 A1, A2 H1 + H2).  So every thread reduces a run of R tokens of two neighbouring channels to (A, H), the
@@ -15,6 +19,7 @@
 // goes through global memory, nothing waits outside the cluster, whose blocks run together, and the order of all
 // operations is fixed by the sizes.
 //
+// (All times here and below: replays of a CUDA graph of 20 calls, inputs larger than L2 except where they are small.)
 // What a step costs is instructions (a value has 6 bytes to move at bf16, about 30 issue slots an SM at full
 // bandwidth): two channels a thread go through the packed fp32 pair arithmetic of sm_100a, tiles come by TMA, and a
 // step has one __syncthreads, which also says that the tile's values are in registers and its place can be filled
@@ -132,7 +137,7 @@ __device__ __forceinline__ void join_warp(Pair& p, Pair& all, int run) {
 //   kTma       one copy of the whole tile by TMA; rows and tensors start on 16 bytes
 //   kByThread  every thread copies what it will read itself, two values or one at a time, asynchronously where they
 //              have 4 bytes at least
-// B=8, T=2048, C=1024 bf16 forward: 23 us by TMA, 30 us by thread; C=1002 31 us; C=1001, one value at a time, 53 us.
+// B=8, T=2048, C=1008 bf16 forward: 22 us by TMA, 31 us by thread; C=1002 31 us; C=1001, one value at a time, 44 us.
 enum Load { kTma = 0, kByThread = 1 };
 
 struct Args {
@@ -546,12 +551,12 @@ bool make_map(CUtensorMap* m, const void* base, long long BH, int T, int D, int 
 
 // How a variant with slabs of 2 LPR channels is cut: blocks of W warps, MINB of them an SM, R tokens a thread, STAGES
 // tiles in shared memory, up to MAXK blocks a cluster.
-// Blocks of 4 warps: 8 warps with the same bytes in flight pay for joining twice the warps (B=8, T=2048, C=2048 bf16
-// forward 45 against 43 us; B=1, T=32768, C=1024: 72 against 57 us).  Forward: 16 tokens a thread, since 8 make twice
-// the joins an element (55 us); one tile of g is 8 KB (16 KB fp32), so three stages of three blocks fit the 227 KB.
-// Backward: the third array and the recomputed states take the registers of the other 8 tokens (with 16, spills: 217
-// against 84 us for the complement), and a tile has to start at a kept state, so slabs of 64 channels would need 8
-// warps: slabs of 32 are its widest (B=8, T=2048, C=2048 bf16 63 against 65 us; fp32 3 x 2 x 1531 x 333: 18 against 21).
+// Blocks of 4 warps: 8 warps with the same bytes in flight pay for joining twice the warps (B=1, T=32768, C=1024 bf16
+// forward a quarter longer).  Forward: 16 tokens a thread, since 8 make twice the joins an element (B=8, T=2048, C=2048
+// a fifth longer); one tile of g is 8 KB (16 KB fp32), so three stages of three blocks fit the 227 KB.
+// Backward: the third array and the recomputed states take the registers of the other 8 tokens (with 16 the complement
+// spills and takes two and a half times as long), and a tile has to start at a kept state, so slabs of 64 channels
+// would need 8 warps: slabs of 32 are its widest (B=8, T=2048, C=2048 bf16 62 against 65 us).
 template <typename T, int LPR, bool BWD>
 struct Shape {
   static_assert(!BWD || LPR < 32, "a tile of the backward starts at a kept state");
@@ -564,7 +569,7 @@ struct Shape {
 // How many blocks share a slab, and what that costs.  A step of a block takes a fixed time, more the more blocks
 // exchange, and the work of a tile times the blocks of the SM, somewhat more for narrower rows (their lanes also join
 // across the warp):
-//     cost = steps (0.3 + 0.08 K + 0.6 (R / 16) blocks_an_sm share)
+//     cost = steps (fixed + 0.08 K + 0.6 (R / 16) blocks_an_sm share)
 // fitted to 34 shapes (both types and directions, 256 to 65,536 tokens, 64 to 16,384 channels in all, every K and
 // slab): what it chooses takes 1.04 times as long as the best choice on average.  K is 1, 2, 3, 4, 6, 8 or 16, all
 // blocks running at once (in between, clusters leave places free: B=1, T=32768, C=1024 forward 65 us with 13, 47 us
@@ -582,7 +587,9 @@ Plan plan(const Args& a, long long BH) {
   typedef Block<T, S::W, LPR, S::R, BWD ? 3 : 2, S::STAGES, S::MAXK, true, LOAD> B;
   constexpr int SHARED = S::STAGES * B::STAGE + S::W * LPR * (BWD ? 48 : 32) + (int)sizeof(typename B::Ex) + 1088;
   constexpr int PLACES = 148 * (S::MINB < 233472 / SHARED ? S::MINB : 233472 / SHARED);  // 228 KB an SM
-  constexpr double share = LPR == 8 ? 1.5 : LPR == 16 && !BWD ? 1.2 : 1.0;
+  // Tiles that the threads copy make a step longer, and short rows off 16 bytes touch more sectors.
+  constexpr double fixed = LOAD == kByThread ? 0.9 : 0.3;
+  constexpr double share = (LPR == 8 ? 1.5 : LPR == 16 && !BWD ? 1.2 : 1.0) * (LOAD == kByThread && LPR < 32 ? 1.25 : 1.0);
   Plan best;
   best.slabs = (a.D + B::CW - 1) / B::CW;
   best.tiles = (int)(((long long)a.T + B::TILE - 1) / B::TILE);
@@ -591,7 +598,7 @@ Plan plan(const Args& a, long long BH) {
     const long long n = best.cols * K;
     if (K > 1 && (K > S::MAXK || K > best.tiles || n > (K < 6 ? PLACES : PLACES / 8 * 7))) break;
     const double c = (double)((best.tiles + K - 1) / K) *
-                     (0.3 + (K > 1 ? 0.08 * K : 0.) + 0.6 * S::R / 16 * (double)((n + 147) / 148) * share);
+                     (fixed + (K > 1 ? 0.08 * K : 0.) + 0.6 * S::R / 16 * (double)((n + 147) / 148) * share);
     if (K == 1 || c < best.cost) best.K = K, best.cost = c;
   }
   return best;
