@@ -10,7 +10,8 @@
 // and y, dx, dz written once.  The mean is subtracted before the squares are summed.  What there is to save is
 // instructions (at full bandwidth a bf16 value has about 30 issue slots forward, 55 backward) and the latency of two
 // dependent row sums: 16 values a lane at bf16, so that D = 512 needs no more than a warp (8 a lane take a third longer
-// forward, an eighth backward), packed fp32 pairs for the arithmetic, and the row of the next step loaded before this one is worked on.
+// forward, an eighth backward), packed fp32 pairs for the arithmetic, and the row of the next step loaded before this
+// one is worked on.
 // A block serves one head and strides over the tokens, so that a lane keeps its channels: w and b are loaded once
 // (the backward keeps them in shared memory), and the sums of dw and db stay in registers until the block ends.  They
 // are then joined over the block's rows, written as one partial row a block, and a second launch adds the partial

@@ -18,8 +18,16 @@ __global__ void __launch_bounds__(1024) join_kernel(const float* part_w, const f
   const int k = threadIdx.x & 31, g = threadIdx.x >> 5, c = blockIdx.x * 32 + k;
   float t = 0.f;
   if (c < cols) {
-#pragma unroll 8
-    for (int r = g; r < rows; r += 32) t += part[(size_t)r * cols + c];
+    for (int first = g; first < rows; first += 32 * 8) {  // eight loads in flight: a row's latency is paid once
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = first + 32 * i;
+        v[i] = r < rows ? part[(size_t)r * cols + c] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t += v[i];
+    }
   }
   s[g][k] = t;
   __syncthreads();
@@ -84,7 +92,8 @@ extern "C" int gla_group_norm_bwd(const void* x, const void* z, const float* w, 
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, join_kernel, (const float*)a.part_w, (const float*)a.part_b, dw, db, rows, cols);
+  const float *part_w = a.part_w, *part_b = a.part_b;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, join_kernel, part_w, part_b, dw, db, rows, cols);
   if (e != cudaSuccess) (void)cudaGetLastError();
   return e == cudaSuccess ? GLA_OK : GLA_ERR_CUDA;
 }

@@ -12,8 +12,8 @@
 // (pi/4)^10 / 10! = 2.5e-8.  So the angle's error is that of the fraction, 2^-54 turns, times the position.
 //
 // Measured (bf16, replays of a CUDA graph of 20 calls): q and k [8, 2048, 4, 256] channels last to head-major 23 us
-// (5.9 TB/s), half as long again with the angles in 64-bit floating point; q, k [1, 8 + 2, 32768, 128], half of it turned,
-// 31 us (5.5 TB/s), two fifths longer when turned and copied vectors were different threads' work; 16 x (8 + 8) x 128,
+// (5.9 TB/s), half as long again with the angles in 64-bit floating point; q, k [1, 8 + 2, 32768, 128], half of it
+// turned, 31 us (5.5 TB/s), two fifths longer when turned and copied vectors were different threads' work; 16 x (8 + 8) x 128,
 // one token, 2.6 us.
 #include <limits.h>
 #include <math.h>

@@ -304,9 +304,9 @@ struct Block {
     if constexpr (CLUSTER) {
       const int s = step & 1;
       if (run == 0) {
-        const float v[4] = {lo(block.A), hi(block.A), lo(block.H), hi(block.H)};
         for (int r = warp; r < a.K; r += W)
-          cl::store_async(cl::peer(sm::smem_u32(&ex.slot[s][rank][lane_c]), r), v, cl::peer(sm::smem_u32(&ex.bar[s]), r));
+          cl::store_async(cl::peer(sm::smem_u32(&ex.slot[s][rank][lane_c]), r), lo(block.A), hi(block.A), lo(block.H),
+                          hi(block.H), cl::peer(sm::smem_u32(&ex.bar[s]), r));
       }
       if (alive) {
         alive = cl::wait(sm::smem_u32(&ex.bar[s]), (step >> 1) & 1, a.latch);
@@ -574,8 +574,8 @@ struct Shape {
 // slab): what it chooses takes 1.04 times as long as the best choice on average.  K is 1, 2, 3, 4, 6, 8 or 16, all
 // blocks running at once (in between, clusters leave places free: B=1, T=32768, C=1024 forward 65 us with 13, 47 us
 // with 8), and clusters of six and more take seven eighths of the places at most, since how they fill the GPU's groups
-// of SMs differs from one GPU to the next (2 x 2 x 3000 x 200 bf16 backward: 16 us with 52 clusters of 8, 13 us with 52 of 6;
-// fp32 3 x 2 x 1531 x 333 forward with 66 of 6: 13 us on one GPU, 18 us on another).
+// of SMs differs from one GPU to the next (2 x 2 x 3000 x 200 bf16 backward: 16 us with 52 clusters of 8, 13 us with
+// 52 of 6; fp32 3 x 2 x 1531 x 333 forward with 66 of 6: 13 us on one GPU, 18 us on another).
 struct Plan {
   long long cols = 0;
   int slabs = 0, tiles = 0, K = 0;
@@ -589,7 +589,8 @@ Plan plan(const Args& a, long long BH) {
   constexpr int PLACES = 148 * (S::MINB < 233472 / SHARED ? S::MINB : 233472 / SHARED);  // 228 KB an SM
   // Tiles that the threads copy make a step longer, and short rows off 16 bytes touch more sectors.
   constexpr double fixed = LOAD == kByThread ? 0.9 : 0.3;
-  constexpr double share = (LPR == 8 ? 1.5 : LPR == 16 && !BWD ? 1.2 : 1.0) * (LOAD == kByThread && LPR < 32 ? 1.25 : 1.0);
+  constexpr double rows = LOAD == kByThread && LPR < 32 ? 1.25 : 1.0;
+  constexpr double share = (LPR == 8 ? 1.5 : LPR == 16 && !BWD ? 1.2 : 1.0) * rows;
   Plan best;
   best.slabs = (a.D + B::CW - 1) / B::CW;
   best.tiles = (int)(((long long)a.T + B::TILE - 1) / B::TILE);

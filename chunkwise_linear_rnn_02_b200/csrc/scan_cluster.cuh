@@ -33,25 +33,13 @@ __device__ __forceinline__ uint32_t peer(uint32_t a, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
   return r;
 }
-// Store N floats in a peer's shared memory; they count 4 N bytes on the peer's mbarrier when they arrive.
-template <int N>
-__device__ __forceinline__ void store_async(uint32_t at, const float (&v)[N], uint32_t bar) {
-  static_assert(N % 2 == 0, "pairs of floats");
-  if constexpr (N % 4 == 0) {
-#pragma unroll
-    for (int i = 0; i < N; i += 4)
-      asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
-                       at + i * 4),
-                   "r"(__float_as_uint(v[i])), "r"(__float_as_uint(v[i + 1])), "r"(__float_as_uint(v[i + 2])),
-                   "r"(__float_as_uint(v[i + 3])), "r"(bar)
-                   : "memory");
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; i += 2)
-      asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(at + i * 4),
-                   "r"(__float_as_uint(v[i])), "r"(__float_as_uint(v[i + 1])), "r"(bar)
-                   : "memory");
-  }
+// Store four floats in a peer's shared memory (16-byte aligned); they count 16 bytes on the peer's mbarrier when they
+// arrive.
+__device__ __forceinline__ void store_async(uint32_t at, float x, float y, float z, float w, uint32_t bar) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(at),
+      "r"(__float_as_uint(x)), "r"(__float_as_uint(y)), "r"(__float_as_uint(z)), "r"(__float_as_uint(w)), "r"(bar)
+      : "memory");
 }
 // Wait (about a second at most, then the latch is set and false returned) for a phase whose data
 // comes from other blocks of the cluster.

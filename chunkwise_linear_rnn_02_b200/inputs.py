@@ -20,7 +20,7 @@ import dataclasses
 
 import torch
 
-__all__ = ["GLAShape", "GSAShape", "CONFIGS", "make_gla_inputs", "make_gsa_inputs"]
+__all__ = ["GLAShape", "GSAShape", "CONFIGS", "make_gla_inputs", "make_gsa_inputs", "make_layer_inputs"]
 
 
 @dataclasses.dataclass(frozen=True)
@@ -98,3 +98,15 @@ def make_gsa_inputs(B, H, T, dk, dv, m, dtype=torch.bfloat16, seed=0, gate_tau=8
     if with_do:
         out["do"] = _randn(gen, (B, H, T, dv))
     return {n: t.to(dtype) for n, t in out.items()}
+
+
+def make_layer_inputs(B, H, T, D, dtype=torch.bfloat16, seed=0, gate_tau=16.0):
+    """CPU tensors for the elementwise scan, the group norm and rotary: g (log-decay), x, do [B,H,T,D] and z, dy
+    [B,T,H,D] in ``dtype``, w, b [H,D] float32."""
+    gen = torch.Generator().manual_seed(seed)
+    out = {"g": torch.nn.functional.logsigmoid(_randn(gen, (B, H, T, D))) / gate_tau}
+    for n, shape in (("x", (B, H, T, D)), ("do", (B, H, T, D)), ("z", (B, T, H, D)), ("dy", (B, T, H, D))):
+        out[n] = _randn(gen, shape)
+    out = {n: t.to(dtype) for n, t in out.items()}
+    out["w"], out["b"] = 1 + 0.1 * _randn(gen, (H, D)), 0.1 * _randn(gen, (H, D))
+    return out
