@@ -18,7 +18,7 @@
 // rows in order (no atomics: the result does not depend on how blocks are scheduled).
 //
 // Measured (replays of a CUDA graph of 20 calls) with gate and weights: B=8, H=4, T=2048, D=512 bf16 forward 36 us
-// (5.6 TB/s), backward 69 us (4.9 TB/s); fp32 72 us (5.6 TB/s) and 130 us (5.2 TB/s); B=8, H=4, D=256, one token 2.1 us.
+// (5.6 TB/s), backward 68 us (4.9 TB/s); fp32 72 us (5.6 TB/s) and 130 us (5.2 TB/s); B=8, H=4, D=256, one token 2.1 us.
 #pragma once
 
 #include <limits.h>
@@ -228,10 +228,9 @@ __global__ void __launch_bounds__(threads_of(LANES), MINB) norm_kernel(const Arg
   };
   load();
   for (long long first = (long long)blockIdx.x * ROWS; first < a.tokens; first += step) {
-    const R px = nx, pz = nz;
-    R pd = nd;
+    R px = nx, pz = nz, pd = nd;
     const bool live = tok < a.tokens;
-    if (BWD && !live) pd.zero();  // nothing of it goes into the sums of dw and db
+    if (BWD && !live) px.zero(), pz.zero(), pd.zero();  // a row that is none adds nothing to the sums of dw and db
     const size_t out = row, xout = xrow;
     tok += step, row += row_step, xrow += x_step;
     if (a.head_major && tok < a.tokens) {

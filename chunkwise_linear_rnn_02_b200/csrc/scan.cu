@@ -176,10 +176,12 @@ struct Block {
   int lane_c, run, warp, c, slab;
   size_t bh;
   uint32_t rank;
-  bool alive, mine0, mine1;
+  int gave_up;  // after a wait has run out, the step whose tile came last or never; kNever before
+  bool mine0, mine1;
+  static constexpr int kNever = INT_MAX;
 
   __device__ __forceinline__ Block(const Args& args, char* smem, uint64_t* bars, Ex& e)
-      : a(args), stage(smem), full(bars), ex(e), alive(true) {
+      : a(args), stage(smem), full(bars), ex(e), gave_up(kNever) {
     const int lane = threadIdx.x & 31;
     lane_c = lane % LPR, run = lane / LPR, warp = threadIdx.x >> 5;
     const uint32_t col = CLUSTER ? blockIdx.x / (uint32_t)a.K : blockIdx.x;
@@ -257,7 +259,7 @@ struct Block {
   __device__ __forceinline__ void prefetch(const Maps& maps, int step, long long tile) {
     char* at = stage + (step % STAGES) * STAGE;
     if constexpr (LOAD == kTma) {
-      if (step < a.steps && alive && threadIdx.x == 0) {
+      if (step < a.steps && gave_up == kNever && threadIdx.x == 0) {
         uint64_t* bar = &full[step % STAGES];
         sm::mbar_arrive_expect_tx(bar, STAGE);
         const int t = tile < 0 || tile > a.T ? a.T : (int)tile;
@@ -274,7 +276,7 @@ struct Block {
   }
   __device__ __forceinline__ void arrived(int step) {
     if constexpr (LOAD == kTma) {
-      if (alive) alive = sm::mbar_wait(&full[step % STAGES], (step / STAGES) & 1, a.latch);
+      if (gave_up == kNever && !sm::mbar_wait(&full[step % STAGES], (step / STAGES) & 1, a.latch)) gave_up = step;
     } else {
       cl::copy_wait<STAGES - 1>();
     }
@@ -308,9 +310,10 @@ struct Block {
           cl::store_async(cl::peer(sm::smem_u32(&ex.slot[s][rank][lane_c]), r), lo(block.A), hi(block.A), lo(block.H),
                           hi(block.H), cl::peer(sm::smem_u32(&ex.bar[s]), r));
       }
-      if (alive) {
-        alive = cl::wait(sm::smem_u32(&ex.bar[s]), (step >> 1) & 1, a.latch);
-        if (alive && threadIdx.x == 0)  // the slot's next use, two steps on
+      if (gave_up == kNever) {
+        if (!cl::wait(sm::smem_u32(&ex.bar[s]), (step >> 1) & 1, a.latch))
+          gave_up = step + 1;
+        else if (threadIdx.x == 0)  // the slot's next use, two steps on
           sm::mbar_arrive_expect_tx(&ex.bar[s], (uint32_t)(a.K * LPR * 16));
       }
       for (int r = 0; r < a.K; ++r) {
@@ -325,6 +328,10 @@ struct Block {
   }
   __device__ __forceinline__ void close(F2 carry) {
     if (a.last && rank == 0 && warp == 0 && run == 0) keep(a.last + bh * a.D + c, carry);
+    // After a wait that ran out, the copies still on their way are waited for, again with a limit.
+    if (LOAD == kTma && gave_up != kNever && threadIdx.x == 0)
+      for (int s = gave_up; s < gave_up + STAGES && s < a.steps; ++s)
+        sm::mbar_wait(&full[s % STAGES], (s / STAGES) & 1, a.latch);
     if constexpr (CLUSTER) cl::sync();  // no block leaves while others may still send to it
   }
 };

@@ -304,8 +304,8 @@ int gla_scan_step(const void* g, const void* x, float* S, void* o, int B, int H,
  *   gla_group_norm_bwd  in : x, z, w, b, dy [B,T,H,D]
  *                       out: dx in `layout`; dz [B,T,H,D] (optional; needs z);
  *                            dw, db [weight_rows, D] fp32 (optional), summed in a fixed order
- * weight_rows: H (a weight for each channel) or 1 (one row shared by the heads).  1 <= D <= 8192
- * (else GLA_ERR_UNSUPPORTED); eps > 0 and finite.  T == 0: dw and db are zeroed, nothing else is
+ * weight_rows: H (a weight for each channel) or 1 (one row shared by the heads).  1 <= D <= 8192,
+ * H <= 65535 and B*T <= 2^31-1 (else GLA_ERR_UNSUPPORTED); eps > 0 and finite.  T == 0: dw and db are zeroed, nothing else is
  * written.  Statistics and sums are fp32.  Workspace of the backward: per-block partial sums of dw
  * and db (0 bytes when neither is asked for).
  * ------------------------------------------------------------------------------------- */
@@ -335,7 +335,7 @@ int gla_group_norm_bwd(const void* x, const void* z, const float* w, const float
  * far positions keep fp32 accuracy; freq has to be finite.  The rotation is fp32 and rounded once.
  * inverse != 0 rotates by -A with the same scale, which is the transpose: the backward of a call is
  * the call with inverse set and the layouts exchanged.  1 <= D <= 8192, R even, 2 <= R <= D; scale
- * finite.  T == 0 enqueues nothing.
+ * finite; B*T and B*T*D/2 at most 2^31 - 512 (else GLA_ERR_UNSUPPORTED).  T == 0 enqueues nothing.
  * ------------------------------------------------------------------------------------- */
 int gla_rotary(const void* q, const void* k, void* qo, void* ko, const double* freq, const long long* pos,
                long long pos0, int pos_rows, int B, int Hq, int Hk, int T, int D, int R, float scale,

@@ -153,6 +153,24 @@ def test_norm_gates_far_out(dtype):
             assert torch.isfinite(t).all()
 
 
+def test_norm_infinite_values_stay_in_their_sums():
+    """A gate that makes dw infinite: the last step's places without a row add nothing to the sums (an infinity there
+    would turn into NaN), and other channels, rows and heads stay finite."""
+    d = make(1, 2, 37, 64, F32, 2, True, "bhtd", seed=11)
+    d["z"][0, 36, 1, 5] = float("inf")  # the last row of head 1
+    d["dy"][0, 36, 1, 5] = 1.0
+    d["x"][0, 1, 36, 5] = 7.0           # n > 0 there
+    c = cuda(d)
+    y = gla.group_norm_fwd(c["x"], c["z"], c["w"], c["b"])
+    assert torch.isinf(y[0, 36, 1, 5]) and torch.isfinite(y[0, :36]).all() and torch.isfinite(y[:, :, 0]).all()
+    dx, dz, dw, db = gla.group_norm_bwd(c["x"], c["dy"], c["z"], c["w"], c["b"])
+    assert dw[1, 5] == float("inf") and db[1, 5] == float("inf")
+    for t in (dw, db):
+        t[1, 5] = 0
+        assert torch.isfinite(t).all()
+    assert torch.isfinite(dx[0, 0]).all() and torch.isfinite(dx[0, 1, :36]).all()
+
+
 def test_norm_empty_and_unaligned():
     x = torch.empty(2, 3, 0, 16, device="cuda", dtype=BF16)
     w = torch.ones(3, 16, device="cuda")

@@ -116,6 +116,26 @@ def test_scan_against_oracle(B, H, T, D, dtype, complement):
     assert gla.device_error() == 0
 
 
+# Each slab width, with one block and with a cluster, by TMA and copied by the threads, in one step and in several.
+VARIANTS = [
+    (1, 1, 200, 16), (16, 4, 257, 72), (300, 1, 130, 33), (3, 4, 513, 200), (3, 4, 1025, 65), (40, 4, 257, 24), (40, 2, 257, 65),
+    (8, 4, 1025, 24), (16, 1, 1025, 65), (40, 4, 513, 16), (300, 1, 513, 7), (1, 1, 20000, 16), (100, 2, 130, 24), (16, 2, 513, 24),
+    (100, 1, 130, 33), (16, 4, 257, 33), (1, 1, 6000, 7), (2, 1, 65, 1001), (4, 1, 1025, 200), (1, 1, 2049, 16),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("complement", [False, True])
+@pytest.mark.parametrize("B,H,T,D", VARIANTS)
+def test_scan_variants_against_oracle(B, H, T, D, dtype, complement):
+    d = make(B, H, T, D, dtype, seed=T * 37 + D, resets=0.001, keeps=0.01)
+    ref, tol = bounds(d, complement, True, True)
+    got = run_all(d, complement)
+    for n in ref:
+        check(n, got[n], ref[n], tol[n], F32 if n in ("hT", "dh0") else dtype)
+    assert gla.device_error() == 0
+
+
 @pytest.mark.parametrize("with_h0,with_dhT", [(False, False), (True, False), (False, True)])
 def test_scan_optional_states(with_h0, with_dhT):
     d = make(2, 2, 200, 48, BF16, seed=5)
