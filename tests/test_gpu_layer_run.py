@@ -79,3 +79,35 @@ def test_scan_layer_prompt_then_tokens(dtype):
     rdo, _, rdw, _ = O.group_norm_bwd(f64(first).reshape(B, T, G, C // G), f64(dy), f64(z[:, :T]), f64(w), None, **how)
     assert_close("do", do, rdo.reshape(B, 1, T, C), tol)
     assert_close("dw", dw, rdw, tol)
+
+
+def test_two_threads_at_once():
+    """The scan's and the norm's backward from two host threads on streams of their own: the bits of each alone."""
+    import threading
+
+    gen = torch.Generator().manual_seed(4)
+    r = lambda *s: torch.randn(*s, generator=gen).to(torch.bfloat16).cuda()  # noqa: E731
+    g, x, do = -r(1, 2, 5000, 64).abs() / 16, r(1, 2, 5000, 64), r(1, 2, 5000, 64)
+    nx, nz, ndy = r(4, 4, 700, 128), r(4, 700, 4, 128), r(4, 700, 4, 128)
+    w, b = torch.randn(4, 128, generator=gen).cuda(), torch.randn(4, 128, generator=gen).cuda()
+    jobs = [lambda: gla.scan_bwd(g, x, do, complement=True), lambda: gla.group_norm_bwd(nx, ndy, nz, w, b)]
+    alone = [job() for job in jobs]
+    torch.cuda.synchronize()
+    got = [None, None]
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(5):
+                out = jobs[i]()
+        s.synchronize()
+        got[i] = out
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(timeout=120)
+    for a, o in zip(alone, got):
+        assert o is not None and all(torch.equal(p, q) for p, q in zip(a, o))
+    assert gla.device_error() == 0
