@@ -3,7 +3,7 @@
 //     h_t = a_t h_{t-1} + b_t,   a_t = exp g_t,   b_t = x_t  or  (1 - a_t) x_t
 //
 // Measured, bf16: B=8, T=2048, C=2048 forward 34 us (5.9 TB/s), backward 62 us (5.4 TB/s), for the complement 39 and
-// 80 us; B=1, T=32768, C=1024 (clusters of eight and six) forward 47 us, backward 91 us; one token of 32 x 2048 1.5 us.
+// 73 us; B=1, T=32768, C=1024 (clusters of eight and six) forward 47 us, backward 91 us; one token of 32 x 2048 1.5 us.
 // fp32, B=8, T=2048, C=2048: 65 us (6.1 TB/s) and 110 us (6.1 TB/s).
 //
 // HBM-bound: g and x are read once and o written once.  A run of tokens acts on the state in front of it as
@@ -567,7 +567,7 @@ bool make_map(CUtensorMap* m, const void* base, long long BH, int T, int D, int 
 template <typename T, int LPR, bool BWD>
 struct Shape {
   static_assert(!BWD || LPR < 32, "a tile of the backward starts at a kept state");
-  static constexpr int W = 4, MINB = BWD && LPR == 16 && sizeof(T) == 2 ? 4 : 3;
+  static constexpr int W = 4, MINB = BWD && sizeof(T) == 2 ? 4 : 3;
   static constexpr int R = BWD || (sizeof(T) == 4 && LPR < 32) ? 8 : 16;
   static constexpr int STAGES = sizeof(T) == 4 && LPR == 32 ? 2 : 3;
   static constexpr int MAXK = LPR == 8 ? 16 : LPR == 16 ? 8 : 6;
@@ -582,13 +582,14 @@ struct Shape {
 // blocks running at once (in between, clusters leave places free: B=1, T=32768, C=1024 forward 65 us with 13, 47 us
 // with 8), and clusters of six and more take seven eighths of the places at most, since how they fill the GPU's groups
 // of SMs differs from one GPU to the next (2 x 2 x 3000 x 200 bf16 backward: 16 us with 52 clusters of 8, 13 us with
-// 52 of 6; fp32 3 x 2 x 1531 x 333 forward with 66 of 6: 13 us on one GPU, 18 us on another).
+// 52 of 6; fp32 3 x 2 x 1531 x 333 forward with 66 of 6: 13 us on one GPU, 18 us on another).  Clusters of 16 serve where
+// they leave an SM no more than a block.
 struct Plan {
   long long cols = 0;
   int slabs = 0, tiles = 0, K = 0;
   double cost = 0.;
 };
-template <typename T, int LPR, int LOAD, bool BWD>
+template <typename T, int LPR, int LOAD, bool COMP, bool BWD>
 Plan plan(const Args& a, long long BH) {
   typedef Shape<T, LPR, BWD> S;
   typedef Block<T, S::W, LPR, S::R, BWD ? 3 : 2, S::STAGES, S::MAXK, true, LOAD> B;
@@ -597,14 +598,16 @@ Plan plan(const Args& a, long long BH) {
   // Tiles that the threads copy make a step longer, and short rows off 16 bytes touch more sectors.
   constexpr double fixed = LOAD == kByThread ? 0.9 : 0.3;
   constexpr double rows = LOAD == kByThread && LPR < 32 ? 1.25 : 1.0;
-  constexpr double share = (LPR == 8 ? 1.5 : LPR == 16 && !BWD ? 1.2 : 1.0) * rows;
+  // (The complement's backward at bf16 spills on the wider slab: B=8, T=2048, C=2048 81 us, 73 us on the narrow one.)
+  constexpr double narrow = BWD && COMP && sizeof(T) == 2 ? 1.15 : 1.5;
+  constexpr double share = (LPR == 8 ? narrow : LPR == 16 && !BWD ? 1.2 : 1.0) * rows;
   Plan best;
   best.slabs = (a.D + B::CW - 1) / B::CW;
   best.tiles = (int)(((long long)a.T + B::TILE - 1) / B::TILE);
   best.cols = BH * best.slabs;
   for (int K : {1, 2, 3, 4, 6, 8, 16}) {
     const long long n = best.cols * K;
-    if (K > 1 && (K > S::MAXK || K > best.tiles || n > (K < 6 ? PLACES : PLACES / 8 * 7))) break;
+    if (K > 1 && (K > S::MAXK || K > best.tiles || n > (K < 6 ? PLACES : K < 16 ? PLACES / 8 * 7 : 148))) break;
     const double c = (double)((best.tiles + K - 1) / K) *
                      (fixed + (K > 1 ? 0.08 * K : 0.) + 0.6 * S::R / 16 * (double)((n + 147) / 148) * share);
     if (K == 1 || c < best.cost) best.K = K, best.cost = c;
@@ -666,9 +669,9 @@ int launch(Args a, const Plan& p, long long BH, cudaStream_t st) {
 // Slabs of 64 (forward), 32 or 16 channels, whichever costs least.
 template <typename T, int LOAD, bool COMP, bool BWD>
 int choose(const Args& a, long long BH, cudaStream_t st) {
-  const Plan mid = plan<T, 16, LOAD, BWD>(a, BH), narrow = plan<T, 8, LOAD, BWD>(a, BH);
+  const Plan mid = plan<T, 16, LOAD, COMP, BWD>(a, BH), narrow = plan<T, 8, LOAD, COMP, BWD>(a, BH);
   if constexpr (!BWD) {
-    const Plan wide = plan<T, 32, LOAD, BWD>(a, BH);
+    const Plan wide = plan<T, 32, LOAD, COMP, BWD>(a, BH);
     if (wide.cost <= mid.cost && wide.cost <= narrow.cost) return launch<T, 32, LOAD, COMP, BWD>(a, wide, BH, st);
   }
   if (mid.cost <= narrow.cost) return launch<T, 16, LOAD, COMP, BWD>(a, mid, BH, st);
