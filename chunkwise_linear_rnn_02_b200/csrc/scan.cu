@@ -3,7 +3,7 @@
 //     h_t = a_t h_{t-1} + b_t,   a_t = exp g_t,   b_t = x_t  or  (1 - a_t) x_t
 //
 // Measured, bf16: B=8, T=2048, C=2048 forward 34 us (5.9 TB/s), backward 62 us (5.4 TB/s), for the complement 39 and
-// 73 us; B=1, T=32768, C=1024 (clusters of eight and six) forward 47 us, backward 91 us; one token of 32 x 2048 1.5 us.
+// 73 us; B=1, T=32768, C=1024 (clusters of eight) forward 47 us, backward 91 us; one token of 32 x 2048 1.5 us.
 // fp32, B=8, T=2048, C=2048: 65 us (6.1 TB/s) and 110 us (6.1 TB/s).
 //
 // HBM-bound: g and x are read once and o written once.  A run of tokens acts on the state in front of it as
@@ -137,7 +137,7 @@ __device__ __forceinline__ void join_warp(Pair& p, Pair& all, int run) {
 //   kTma       one copy of the whole tile by TMA; rows and tensors start on 16 bytes
 //   kByThread  every thread copies what it will read itself, two values or one at a time, asynchronously where they
 //              have 4 bytes at least
-// B=8, T=2048, C=1008 bf16 forward: 22 us by TMA, 31 us by thread; C=1002 31 us; C=1001, one value at a time, 44 us.
+// B=8, T=2048, C=1008 bf16 forward: 20 us by TMA; by thread, C=1002 31 us, C=1001, one value at a time, 44 us.
 enum Load { kTma = 0, kByThread = 1 };
 
 struct Args {
@@ -559,8 +559,10 @@ bool make_map(CUtensorMap* m, const void* base, long long BH, int T, int D, int 
 // How a variant with slabs of 2 LPR channels is cut: blocks of W warps, MINB of them an SM, R tokens a thread, STAGES
 // tiles in shared memory, up to MAXK blocks a cluster.
 // Blocks of 4 warps: 8 warps with the same bytes in flight pay for joining twice the warps (B=1, T=32768, C=1024 bf16
-// forward a quarter longer).  Forward: 16 tokens a thread, since 8 make twice the joins an element (B=8, T=2048, C=2048
-// a fifth longer); one tile of g is 8 KB (16 KB fp32), so three stages of three blocks fit the 227 KB.
+// forward a quarter longer).  Forward: 16 tokens a thread at bf16, since 8 make twice the joins an element (B=8, T=2048,
+// C=2048 a fifth longer); one tile of g is 8 KB, so three stages of three blocks fit the 227 KB.  fp32 has 8 tokens for
+// the same 8 KB; on slabs of 64 channels it has 16 and two stages of 16 KB, which serves many channels by TMA (B=8,
+// T=2048, C=2048 65 us, 73 us on slabs of 32) and is too little in flight where the threads copy (C=1002 60 and 39 us).
 // Backward: the third array and the recomputed states take the registers of the other 8 tokens (with 16 the complement
 // spills and takes two and a half times as long), and a tile has to start at a kept state, so slabs of 64 channels
 // would need 8 warps: slabs of 32 are its widest (B=8, T=2048, C=2048 bf16 62 against 65 us).
@@ -574,16 +576,30 @@ struct Shape {
 };
 
 // How many blocks share a slab, and what that costs.  A step of a block takes a fixed time, more the more blocks
-// exchange, and the work of a tile times the blocks of the SM, somewhat more for narrower rows (their lanes also join
-// across the warp):
-//     cost = steps (fixed + 0.08 K + 0.6 (R / 16) blocks_an_sm share)
-// fitted to 34 shapes (both types and directions, 256 to 65,536 tokens, 64 to 16,384 channels in all, every K and
-// slab): what it chooses takes 1.04 times as long as the best choice on average.  K is 1, 2, 3, 4, 6, 8 or 16, all
-// blocks running at once (in between, clusters leave places free: B=1, T=32768, C=1024 forward 65 us with 13, 47 us
-// with 8), and clusters of six and more take seven eighths of the places at most, since how they fill the GPU's groups
-// of SMs differs from one GPU to the next (2 x 2 x 3000 x 200 bf16 backward: 16 us with 52 clusters of 8, 13 us with
-// 52 of 6; fp32 3 x 2 x 1531 x 333 forward with 66 of 6: 13 us on one GPU, 18 us on another).  Clusters of 16 serve where
-// they leave an SM no more than a block.
+// exchange, and the work of a tile times the blocks of the SM, which differs with the width of the slab (narrow rows
+// also join across the warp; the complement's backward at bf16 spills on the wider slab):
+//     cost = steps (fixed + block K + work (R / 16) blocks_an_sm)
+// fitted to 54 shapes with every K and slab (both types, 256 to 65,536 tokens, 64 to 6,400 channels in all, rows on
+// 16 bytes, even and odd): what it chooses takes 1.02 times as long as the best choice on average (with one row of
+// constants for all, 1.05 times).
+// K is 1, 2, 3, 4, 6, 8 or 16, all blocks running at once (in between, clusters leave places free: B=1, T=32768, C=1024
+// forward 65 us with 13, 47 us with 8), and clusters of six and more take seven eighths of the places at most, since how
+// they fill the GPU's groups of SMs differs from one GPU to the next (2 x 2 x 3000 x 200 bf16 backward: 16 us with 52
+// clusters of 8, 13 us with 52 of 6; fp32 3 x 2 x 1531 x 333 forward with 66 of 6: 13 us on one GPU, 18 us on another).
+// Clusters of 16 serve where they leave an SM no more than a block.
+struct Cost {
+  double fixed, block, work64, work32, work16;
+};
+template <bool BF16, int LOAD, bool COMP, bool BWD>
+constexpr Cost cost() {
+  if (LOAD == kTma) {
+    if (!BWD) return BF16 ? Cost{0.3, 0.15, 0.6, 0.72, 1.1} : Cost{0.6, 0.08, 0.6, 0.6, 0.9};
+    if (!BF16) return {0.3, 0.11, 0., 0.7, 0.9};
+    return COMP ? Cost{0.6, 0.08, 0., 0.7, 0.69} : Cost{0.6, 0.05, 0., 0.5, 0.75};
+  }
+  if (BF16) return {0.9, 0.08, 0.6, 0.75, BWD ? 1.125 : 1.3};
+  return BWD ? Cost{0.4, 0.08, 0., 0.9, 1.6} : Cost{0.5, 0.08, 0., 0.9, 1.5};
+}
 struct Plan {
   long long cols = 0;
   int slabs = 0, tiles = 0, K = 0;
@@ -595,12 +611,8 @@ Plan plan(const Args& a, long long BH) {
   typedef Block<T, S::W, LPR, S::R, BWD ? 3 : 2, S::STAGES, S::MAXK, true, LOAD> B;
   constexpr int SHARED = S::STAGES * B::STAGE + S::W * LPR * (BWD ? 48 : 32) + (int)sizeof(typename B::Ex) + 1088;
   constexpr int PLACES = 148 * (S::MINB < 233472 / SHARED ? S::MINB : 233472 / SHARED);  // 228 KB an SM
-  // Tiles that the threads copy make a step longer, and short rows off 16 bytes touch more sectors.
-  constexpr double fixed = LOAD == kByThread ? 0.9 : 0.3;
-  constexpr double rows = LOAD == kByThread && LPR < 32 ? 1.25 : 1.0;
-  // (The complement's backward at bf16 spills on the wider slab: B=8, T=2048, C=2048 81 us, 73 us on the narrow one.)
-  constexpr double narrow = BWD && COMP && sizeof(T) == 2 ? 1.15 : 1.5;
-  constexpr double share = (LPR == 8 ? narrow : LPR == 16 && !BWD ? 1.2 : 1.0) * rows;
+  constexpr Cost C = cost<sizeof(T) == 2, LOAD, COMP, BWD>();
+  constexpr double work = (LPR == 32 ? C.work64 : LPR == 16 ? C.work32 : C.work16) * S::R / 16;
   Plan best;
   best.slabs = (a.D + B::CW - 1) / B::CW;
   best.tiles = (int)(((long long)a.T + B::TILE - 1) / B::TILE);
@@ -609,7 +621,7 @@ Plan plan(const Args& a, long long BH) {
     const long long n = best.cols * K;
     if (K > 1 && (K > S::MAXK || K > best.tiles || n > (K < 6 ? PLACES : K < 16 ? PLACES / 8 * 7 : 148))) break;
     const double c = (double)((best.tiles + K - 1) / K) *
-                     (fixed + (K > 1 ? 0.08 * K : 0.) + 0.6 * S::R / 16 * (double)((n + 147) / 148) * share);
+                     (C.fixed + (K > 1 ? C.block * K : 0.) + work * (double)((n + 147) / 148));
     if (K == 1 || c < best.cost) best.K = K, best.cost = c;
   }
   return best;
@@ -666,11 +678,11 @@ int launch(Args a, const Plan& p, long long BH, cudaStream_t st) {
   return GLA_OK;
 }
 
-// Slabs of 64 (forward), 32 or 16 channels, whichever costs least.
+// Slabs of 64 (forward, but not fp32 copied by the threads), 32 or 16 channels, whichever costs least.
 template <typename T, int LOAD, bool COMP, bool BWD>
 int choose(const Args& a, long long BH, cudaStream_t st) {
   const Plan mid = plan<T, 16, LOAD, COMP, BWD>(a, BH), narrow = plan<T, 8, LOAD, COMP, BWD>(a, BH);
-  if constexpr (!BWD) {
+  if constexpr (!BWD && (sizeof(T) == 2 || LOAD == kTma)) {
     const Plan wide = plan<T, 32, LOAD, COMP, BWD>(a, BH);
     if (wide.cost <= mid.cost && wide.cost <= narrow.cost) return launch<T, 32, LOAD, COMP, BWD>(a, wide, BH, st);
   }

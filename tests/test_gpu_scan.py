@@ -136,6 +136,15 @@ def test_scan_variants_against_oracle(B, H, T, D, dtype, complement):
     assert gla.device_error() == 0
 
 
+# Many rows of few channels: widths and loads that fill the GPU without a cluster, or with a small one.
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("complement", [False, True])
+@pytest.mark.parametrize("B,H,T,D", [(150, 1, 130, 33), (40, 2, 130, 72), (300, 1, 130, 16), (40, 2, 64, 24),
+                                     (40, 1, 130, 24), (100, 1, 513, 16), (300, 1, 130, 64)])
+def test_scan_variants_of_many_rows_against_oracle(B, H, T, D, dtype, complement):
+    test_scan_variants_against_oracle(B, H, T, D, dtype, complement)
+
+
 @pytest.mark.parametrize("with_h0,with_dhT", [(False, False), (True, False), (False, True)])
 def test_scan_optional_states(with_h0, with_dhT):
     d = make(2, 2, 200, 48, BF16, seed=5)
