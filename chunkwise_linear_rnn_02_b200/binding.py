@@ -419,8 +419,8 @@ def scan_fwd(g, x, h0=None, complement: bool = False, output_final_state: bool =
     gp, xp = _operand("g", g, g.dtype, g.shape, dev), _operand("x", x, g.dtype, g.shape, dev)
     hp = _operand("h0", h0, torch.float32, (B, H, D), dev)
     o = torch.empty_like(g)
-    hT = torch.empty(B, H, D, dtype=torch.float32, device=dev) if output_final_state else None
-    hc = torch.empty(B, H, -(-T // SCAN_KEEP), D, dtype=torch.float32, device=dev) if save_states else None
+    hT = g.new_empty((B, H, D), dtype=torch.float32) if output_final_state else None
+    hc = g.new_empty((B, H, -(-T // SCAN_KEEP), D), dtype=torch.float32) if save_states else None
     _enqueue("gla_scan_fwd", dev, gp, xp, hp, o.data_ptr(), _address(hT), _address(hc), B, H, T, D, complement, dt)
     return o, hT, hc
 
@@ -435,7 +435,7 @@ def scan_bwd(g, x, do, h0=None, dhT=None, hc=None, complement: bool = False, nee
     dhp = _operand("dhT", dhT, torch.float32, (B, H, D), dev)
     hcp = _operand("hc", hc, torch.float32, (B, H, -(-T // SCAN_KEEP), D), dev)
     dg, dx = torch.empty_like(g), torch.empty_like(g)
-    dh0 = torch.empty(B, H, D, dtype=torch.float32, device=dev) if need_dh0 else None
+    dh0 = g.new_empty((B, H, D), dtype=torch.float32) if need_dh0 else None
     ws, nb = (None, 0)
     if hc is None:
         ws, nb = _workspace(_bytes("gla_scan_bwd_workspace", B, H, T, D, 0), dev)
@@ -497,7 +497,7 @@ def group_norm_fwd(x, z=None, w=None, b=None, kind: str = "group", act: str = "s
     """
     dt, dev, out, rows, xp, zp, wp, bp, kind, act, lay = _norm_args(x, z, w, b, kind, act, layout)
     B, T, H, D = out
-    y = torch.empty(out, dtype=x.dtype, device=dev) if z is None else torch.empty_like(z)
+    y = x.new_empty(out) if z is None else torch.empty_like(z)
     _enqueue("gla_group_norm_fwd", dev, xp, zp, wp, bp, y.data_ptr(), B, H, T, D, rows, kind, act, eps, lay, dt)
     return y
 
@@ -582,9 +582,9 @@ def _rotary(q, k, freq, pos, pos0, interleaved, scale, inverse, in_layout, out_l
         if k is not None:
             ko = torch.empty_like(k)
     else:
-        qo = torch.empty((B, T, Hq, D) if lout else (B, Hq, T, D), dtype=dtype, device=dev)
+        qo = q.new_empty((B, T, Hq, D) if lout else (B, Hq, T, D))
         if k is not None:
-            ko = torch.empty((B, T, Hk, D) if lout else (B, Hk, T, D), dtype=dtype, device=dev)
+            ko = k.new_empty((B, T, Hk, D) if lout else (B, Hk, T, D))
     _enqueue("gla_rotary", dev, qp, kp, qo.data_ptr(), _address(ko), fp, pp, pos0, rows, B, Hq, Hk, T, D,
              2 * freq.shape[0], scale, interleaved, inverse, lin, lout, dt)
     return qo, ko
