@@ -112,6 +112,13 @@ def test_norm_every_mode_without_weights(kind, act, gate):
     check_all(make(2, 3, 19, 64, BF16, 0, gate, "bhtd", seed=3), how, BF16)
 
 
+@pytest.mark.parametrize("kind", ["group", "rms"])
+def test_norm_many_rows_of_a_warp(kind):
+    """Rows of 1,024 values without a gate are one warp's; more of them than the GPU holds at once."""
+    how = dict(kind=kind, act="silu", eps=1e-3, layout="bthd")
+    check_all(make(1, 1, 6001, 1024, BF16, 1, False, "bthd", seed=11), how, BF16)
+
+
 def test_norm_one_weight_alone():
     d = cuda(make(2, 3, 10, 64, F32, 3, True, "bhtd", seed=4))
     _, _, dw, db = gla.group_norm_bwd(d["x"], d["dy"], d["z"], d["w"], d["b"])
