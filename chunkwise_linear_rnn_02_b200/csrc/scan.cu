@@ -614,7 +614,7 @@ Plan plan(const Args& a, long long BH) {
   constexpr Cost C = cost<sizeof(T) == 2, LOAD, COMP, BWD>();
   constexpr double work = (LPR == 32 ? C.work64 : LPR == 16 ? C.work32 : C.work16) * S::R / 16;
   Plan best;
-  best.slabs = (a.D + B::CW - 1) / B::CW;
+  best.slabs = (a.D - 1) / B::CW + 1;  // D goes up to 2^31 - 1
   best.tiles = (int)(((long long)a.T + B::TILE - 1) / B::TILE);
   best.cols = BH * best.slabs;
   for (int K : {1, 2, 3, 4, 6, 8, 16}) {
