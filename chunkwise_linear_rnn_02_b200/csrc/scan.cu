@@ -57,39 +57,67 @@ using gla::Two;
 namespace cl = gla::cluster;
 namespace sm = gla::sm100;
 
-constexpr int kKeep = 64;          // tokens between the kept states
+constexpr int kKeep = 64;  // tokens between the kept states
+constexpr float kLog2e = gla::fast::kLog2e;
+constexpr double kLn2Exact = 0.693147180559945309417;
+constexpr float kLn2 = (float)kLn2Exact, kLn2Rest = (float)(kLn2Exact - (double)kLn2);
 
 __device__ __forceinline__ F2 shfl2(F2 a, int src) {
   return f2(__shfl_sync(0xffffffffu, lo(a), src), __shfl_sync(0xffffffffu, hi(a), src));
 }
 
-// a = exp g and, with REST, 1 - a.  Near g = 0 both come from exp g - 1 = g (1 + g/2 (1 + g/3 (...))), so that
-// neither the 1 - a of a slow gate nor a long product of a's loses its leading digits.  Five terms do up to |g| = 1/8
-// (what is left out, g^5/720 of it, is below 2^-24), where 1 - e^g keeps enough digits; for a alone at bf16 three terms
-// do up to 1/32 (g^4/24 < 2^-24).  Elsewhere a state forgets within a few tokens (8; 32), and the 2^-22 of the
-// approximate exponential has no time to add up.
+__device__ __forceinline__ float max_nan(float x, float y) {  // NaN where either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
+
+// x -> (e^x - 1) / x for |x| <= ln 2 / 2 by a polynomial with c0 = 1 and the coefficients that keep its largest relative error
+// smallest, 2^-25.8 (found by Lawson's reweighted least squares, rounded to fp32).
+__device__ __forceinline__ F2 rise(F2 x) {
+  F2 t = fma2(x, f2(0.0013882521f), f2(0.0083665224f));
+  t = fma2(x, t, f2(0.0416672006f));
+  t = fma2(x, t, f2(0.1666654348f));
+  t = fma2(x, t, f2(0.4999999702f));
+  return fma2(x, t, f2(1.f));
+}
+
+// a = exp g and, with REST, 1 - a.  Neither the 1 - a of a slow gate nor a long product of a's may lose its leading digits,
+// so that near g = 0 both come from exp g - 1.
+//   fp32   g = n ln 2 + f with n whole and |f| <= ln 2 / 2 (the reduction of Cody and Waite), s = 2^n, p = exp f - 1:
+//          a = s + s p is off by 2.5 2^-24 and 1 - a = (1 - s) - s p, which is -p for n = 0, by 5 2^-24, however strong the gate.
+//          n is in the low bits of a sum with 2^23 + 2^22 + 127; these, moved up, are s.  From g = -88 on (and where a would be
+//          below 2^-126) n is -127 and s zero.
+//   bf16   the approximate exponential, off by 2^-22 and by |g| 2^-24 for its argument, but near 0 the series
+//          g (1 + g/2 (1 + g/3 (...))): with REST five terms for |g| < 1/8 (what is left out, g^5/720 of it, is below 2^-24),
+//          for a alone three for |g| < 1/32 (g^4/24 < 2^-24).
 template <typename T, bool REST>
 __device__ __forceinline__ F2 decay(F2 g, F2* rest) {
-  constexpr bool FIVE = REST || sizeof(T) == 4;
-  F2 t;
-  if constexpr (FIVE) {
-    t = fma2(g, f2(1.f / 120.f), f2(1.f / 24.f));
-    t = fma2(g, t, f2(1.f / 6.f));
+  if constexpr (sizeof(T) == 4) {
+    constexpr float kWhole = 12582912.f + 127.f;
+    g = f2(max_nan(lo(g), -88.f), max_nan(hi(g), -88.f));
+    const F2 r = fma2(g, f2(kLog2e), f2(kWhole)), n = add2(r, f2(-kWhole));
+    const F2 f = fma2(n, f2(-kLn2Rest), fma2(n, f2(-kLn2), g)), t = rise(f);
+    const F2 s = f2(__uint_as_float(__float_as_uint(lo(r)) << 23), __uint_as_float(__float_as_uint(hi(r)) << 23));
+    const F2 sf = mul2(s, f);
+    if constexpr (!REST) return fma2(sf, t, s);
+    const F2 sp = mul2(sf, t);
+    *rest = fma2(sp, f2(-1.f), fma2(s, f2(-1.f), f2(1.f)));
+    return add2(s, sp);
   } else {
-    t = f2(1.f / 6.f);
+    constexpr float kNear = REST ? 0.125f : 0.03125f;
+    F2 t = f2(1.f / 6.f);
+    if constexpr (REST) t = fma2(g, fma2(g, f2(1.f / 120.f), f2(1.f / 24.f)), t);
+    t = fma2(g, fma2(g, t, f2(0.5f)), f2(1.f));
+    const F2 near = fma2(t, g, f2(1.f));
+    const F2 y = mul2(g, f2(kLog2e)), far = f2(gla::fast_ex2(lo(y)), gla::fast_ex2(hi(y)));
+    const bool s0 = fabsf(lo(g)) < kNear, s1 = fabsf(hi(g)) < kNear;
+    if constexpr (REST) {
+      const F2 rn = mul2(t, mul2(g, f2(-1.f))), rf = fma2(far, f2(-1.f), f2(1.f));
+      *rest = f2(s0 ? lo(rn) : lo(rf), s1 ? hi(rn) : hi(rf));
+    }
+    return f2(s0 ? lo(near) : lo(far), s1 ? hi(near) : hi(far));
   }
-  t = fma2(g, t, f2(0.5f));
-  t = fma2(g, t, f2(1.f));
-  const F2 near = fma2(t, g, f2(1.f));
-  const F2 y = mul2(g, f2(gla::fast::kLog2e));
-  const F2 far = f2(gla::fast_ex2(lo(y)), gla::fast_ex2(hi(y)));
-  constexpr float kNear = FIVE ? 0.125f : 0.03125f;
-  const bool s0 = fabsf(lo(g)) < kNear, s1 = fabsf(hi(g)) < kNear;
-  if constexpr (REST) {
-    const F2 rn = mul2(t, mul2(g, f2(-1.f))), rf = fma2(far, f2(-1.f), f2(1.f));
-    *rest = f2(s0 ? lo(rn) : lo(rf), s1 ? hi(rn) : hi(rf));
-  }
-  return f2(s0 ? lo(near) : lo(far), s1 ? hi(near) : hi(far));
 }
 
 // The action h -> A h + H of a run on two channels.
