@@ -72,13 +72,21 @@ __device__ __forceinline__ float max_nan(float x, float y) {  // NaN where eithe
   return r;
 }
 
-// x -> (e^x - 1) / x for |x| <= ln 2 / 2 by a polynomial with c0 = 1 and the coefficients that keep its largest relative error
-// smallest, 2^-25.8 (found by Lawson's reweighted least squares, rounded to fp32).
+// x -> (e^x - 1) / x by a polynomial with c0 = 1 and the coefficients that keep its largest relative error smallest (found by
+// Lawson's reweighted least squares, rounded to fp32): 2^-25.8 for |x| <= ln 2 / 2 (WIDE), 2^-23.3 for -1/2 <= x <= 0.
+template <bool WIDE>
 __device__ __forceinline__ F2 rise(F2 x) {
-  F2 t = fma2(x, f2(0.0013882521f), f2(0.0083665224f));
-  t = fma2(x, t, f2(0.0416672006f));
-  t = fma2(x, t, f2(0.1666654348f));
-  t = fma2(x, t, f2(0.4999999702f));
+  F2 t;
+  if constexpr (WIDE) {
+    t = fma2(x, f2(0.0013882521f), f2(0.0083665224f));
+    t = fma2(x, t, f2(0.0416672006f));
+    t = fma2(x, t, f2(0.1666654348f));
+    t = fma2(x, t, f2(0.4999999702f));
+  } else {
+    t = fma2(x, f2(0.0068076085f), f2(0.0410424843f));
+    t = fma2(x, t, f2(0.1665636003f));
+    t = fma2(x, t, f2(0.4999946356f));
+  }
   return fma2(x, t, f2(1.f));
 }
 
@@ -88,16 +96,16 @@ __device__ __forceinline__ F2 rise(F2 x) {
 //          a = s + s p is off by 2.5 2^-24 and 1 - a = (1 - s) - s p, which is -p for n = 0, by 5 2^-24, however strong the gate.
 //          n is in the low bits of a sum with 2^23 + 2^22 + 127; these, moved up, are s.  From g = -88 on (and where a would be
 //          below 2^-126) n is -127 and s zero.
-//   bf16   the approximate exponential, off by 2^-22 and by |g| 2^-24 for its argument, but near 0 the series
-//          g (1 + g/2 (1 + g/3 (...))): with REST five terms for |g| < 1/8 (what is left out, g^5/720 of it, is below 2^-24),
-//          for a alone three for |g| < 1/32 (g^4/24 < 2^-24).
+//   bf16   the approximate exponential, off by 2^-22 and by |g| 2^-24 for its argument, but near 0 the polynomial: with REST for
+//          |g| < 1/2, since beyond it a / (1 - a) < 1.55 and 1 - a is off by 2^-20.8 at most; for a alone for |g| < 1/32, where
+//          three terms of the series do (g^4/24 < 2^-24).  (As at fp32 it takes a fifteenth longer, B=8, T=2048, C=2048 forward.)
 template <typename T, bool REST>
 __device__ __forceinline__ F2 decay(F2 g, F2* rest) {
   if constexpr (sizeof(T) == 4) {
     constexpr float kWhole = 12582912.f + 127.f;
     g = f2(max_nan(lo(g), -88.f), max_nan(hi(g), -88.f));
     const F2 r = fma2(g, f2(kLog2e), f2(kWhole)), n = add2(r, f2(-kWhole));
-    const F2 f = fma2(n, f2(-kLn2Rest), fma2(n, f2(-kLn2), g)), t = rise(f);
+    const F2 f = fma2(n, f2(-kLn2Rest), fma2(n, f2(-kLn2), g)), t = rise<true>(f);
     const F2 s = f2(__uint_as_float(__float_as_uint(lo(r)) << 23), __uint_as_float(__float_as_uint(hi(r)) << 23));
     const F2 sf = mul2(s, f);
     if constexpr (!REST) return fma2(sf, t, s);
@@ -105,11 +113,8 @@ __device__ __forceinline__ F2 decay(F2 g, F2* rest) {
     *rest = fma2(sp, f2(-1.f), fma2(s, f2(-1.f), f2(1.f)));
     return add2(s, sp);
   } else {
-    constexpr float kNear = REST ? 0.125f : 0.03125f;
-    F2 t = f2(1.f / 6.f);
-    if constexpr (REST) t = fma2(g, fma2(g, f2(1.f / 120.f), f2(1.f / 24.f)), t);
-    t = fma2(g, fma2(g, t, f2(0.5f)), f2(1.f));
-    const F2 near = fma2(t, g, f2(1.f));
+    constexpr float kNear = REST ? 0.5f : 0.03125f;
+    const F2 t = REST ? rise<false>(g) : fma2(g, fma2(g, f2(1.f / 6.f), f2(0.5f)), f2(1.f)), near = fma2(t, g, f2(1.f));
     const F2 y = mul2(g, f2(kLog2e)), far = f2(gla::fast_ex2(lo(y)), gla::fast_ex2(hi(y)));
     const bool s0 = fabsf(lo(g)) < kNear, s1 = fabsf(hi(g)) < kNear;
     if constexpr (REST) {

@@ -38,7 +38,10 @@ def relative(got, ref):
 #          sum's u, 3.9 u.  For smaller n it is 1 - a with more of the 1.  The product with x is u more: below 6 u.
 #   a      0.41 * 2.4 u / 1.41 (or 0.3 * 2.4 u / 0.7), u / 2 from f, u from the sum, u from the product with what it
 #          scales: 3.5 u, however strong the gate.
-SHARE, FACTOR = 6 * 2.0 ** -24, 2.0 ** -22
+# bf16 gates: below 1/2 the polynomial is off by 1.5 u, the rest as above; from 1/2 on 1 - a has a's 4 u (the base-2
+# exponential) and 1.25 |g| u (its argument) a / (1 - a) = 1.55 times or less, 7.2 u, and u / 2 / 0.39 of its own, and the product
+# with x u: 9.5 u.
+SHARE, FACTOR, SHARE_BF16 = 6 * 2.0 ** -24, 2.0 ** -22, 2.0 ** -20.7
 RANGES = [(-0.01, -1e-4), (-0.125, -0.01), (-0.5, -0.125), (-4.0, -0.5), (-80.0, -4.0)]
 
 
@@ -58,6 +61,20 @@ def test_share_of_the_complement(lo, hi, form):
     else:  # dx = (1 - a) d, with x in the place of dO
         got = gla.scan_bwd(c[0], torch.zeros_like(c[1]), c[1], complement=True)[1]
     assert relative(got, ref) <= SHARE
+
+
+@pytest.mark.parametrize("lo,hi", RANGES)
+@pytest.mark.parametrize("step", [False, True])
+def test_share_of_the_complement_in_a_state_of_bf16_gates(lo, hi, step):
+    """The state is fp32 whatever the type of the gates."""
+    g, x = span(lo, hi).to(torch.bfloat16), ones(1).to(torch.bfloat16)
+    ref = (-np.expm1(f64(g)) * f64(x))[:, :, 0]
+    if step:
+        got = torch.zeros(1, 1, N, device="cuda")
+        gla.scan_step(g[:, :, 0].cuda(), x[:, :, 0].cuda(), got, complement=True)
+    else:
+        got = gla.scan_fwd(g.cuda(), x.cuda(), complement=True)[1]
+    assert relative(got, ref) <= SHARE_BF16
 
 
 @pytest.mark.parametrize("lo,hi", RANGES)
