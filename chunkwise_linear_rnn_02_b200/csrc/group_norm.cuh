@@ -45,22 +45,33 @@ struct Args {
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2eRest = (float)(1.4426950408889634074 - (double)kLog2e), kLn2 = 0.6931471805599453f;
 
-// 1 / (1 + e^-v) by the approximate exponential and reciprocal: off by 2^-22 or so of itself, and by |v| 2^-24 more where
-// it is small for a far v.  (fp32 gates through the exact ones cost a quarter of the forward's time.)
+// 1 / (1 + e^-v) by the approximate base-2 exponential, off by 2^-22, and reciprocal, off by 2^-23.  The exponential's argument
+// -y, y = v log2 e, is rounded, which costs |v| 2^-24 of e^-v.  At bf16 that is far below the gate's own 2^-9.  At fp32 what y
+// takes too much, r (exact by a fused multiply-add, and the rest of log2 e), is put back as 2^r = 1 + r ln 2 (r^2 is below
+// 2^-32), so that the sigmoid is off by 2^-21 for every v.  (r is no number, or infinite, where y is infinite; 1, and below zero
+// any r, then leaves the sigmoid at 0 or 1.)
+template <typename T>
 __device__ __forceinline__ F2 sigmoid2(F2 v) {
-  const F2 y = mul2(v, f2(-kLog2e));
-  const F2 q = add2(f2(fast_ex2(lo(y)), fast_ex2(hi(y))), f2(1.f));
+  const F2 y = mul2(v, f2(kLog2e)), e = f2(fast_ex2(-lo(y)), fast_ex2(-hi(y)));
+  F2 q;
+  if constexpr (sizeof(T) == 4) {
+    const F2 r = fma2(v, f2(-kLog2eRest), fma2(v, f2(-kLog2e), y));
+    q = fma2(e, fma2(f2(fminf(lo(r), 1.f), fminf(hi(r), 1.f)), f2(kLn2), f2(1.f)), f2(1.f));
+  } else {
+    q = add2(e, f2(1.f));
+  }
   return f2(fast_rcp(lo(q)), fast_rcp(hi(q)));
 }
 // act(v) and its derivative.
-template <int ACT>
+template <typename T, int ACT>
 __device__ __forceinline__ F2 act2(F2 v, F2* slope) {
   if constexpr (ACT == GLA_ACT_NONE) {
     *slope = f2(1.f);
     return v;
   } else {
-    const F2 s = sigmoid2(v), rest = fma2(s, f2(-1.f), f2(1.f));
+    const F2 s = sigmoid2<T>(v), rest = fma2(s, f2(-1.f), f2(1.f));
     if constexpr (ACT == GLA_ACT_SIGMOID) {
       *slope = mul2(s, rest);
       return s;
@@ -270,7 +281,7 @@ __global__ void __launch_bounds__(threads_of(LANES), MINB) norm_kernel(const Arg
       for (int p = 0; p < P; ++p) {
         F2 slope;
         const F2 u = fma2(mul2(c[p], f2(rstd)), w_of(p), b_of(p));
-        o.set(p, GATE ? mul2(u, act2<ACT>(pz.get(p), &slope)) : act2<ACT>(u, &slope));
+        o.set(p, GATE ? mul2(u, act2<T, ACT>(pz.get(p), &slope)) : act2<T, ACT>(u, &slope));
       }
       if (live) o.store((T*)a.y + out, lane, D);
     } else {
@@ -280,10 +291,10 @@ __global__ void __launch_bounds__(threads_of(LANES), MINB) norm_kernel(const Arg
         const F2 n = mul2(c[p], f2(rstd)), w = w_of(p), u = fma2(n, w, b_of(p)), d = pd.get(p);
         F2 slope, du;
         if constexpr (GATE) {
-          du = mul2(d, act2<ACT>(pz.get(p), &slope));
+          du = mul2(d, act2<T, ACT>(pz.get(p), &slope));
           o.set(p, mul2(mul2(d, u), slope));
         } else {
-          act2<ACT>(u, &slope);
+          act2<T, ACT>(u, &slope);
           du = mul2(d, slope);
         }
         sw[p] = fma2(du, n, sw[p]);
