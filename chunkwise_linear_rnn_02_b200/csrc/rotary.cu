@@ -5,11 +5,12 @@
 // their pairs once and applies them to several heads of q and k, whose vectors it loads two heads at a time.  In the
 // half layout the two vectors are the first and the second halves of V pairs; in the interleaved one they are
 // neighbours.  Copied vectors go the same way without the rotation.
-// The angle: freq_i / 2 pi, less its whole turns, becomes a 64-bit fraction once a block; its product with the
-// position, whose overflow drops exactly the whole turns, has the angle's part of a turn in its upper word.  (64-bit
-// floating point for every token took most of the kernel's time.)  The word's upper bits, rounded, are the quadrant; the
-// rest, at most 1/8 turn, goes into the Taylor sums of sine and cosine, to x^9 and x^8: what is left out is below
-// (pi/4)^10 / 10! = 2.5e-8.  So the angle's error is that of the fraction, 2^-54 turns, times the position.
+// The angle: |freq_i| / 2 pi, less its whole turns, becomes a 64-bit fraction once a block (and is negated for a negative
+// frequency); its product with the position, whose overflow drops exactly the whole turns, rounded to the upper word, is the
+// angle's part of a turn.  (64-bit floating point for every token took most of the kernel's time.)  The word's upper bits,
+// rounded, are the quadrant; the rest, at most 1/8 turn, goes into the Taylor sums of sine and cosine, to x^9 and x^8: what is
+// left out is below (pi/4)^10 / 10! = 2.5e-8.  So the angle is off by |p freq| 2^-52 radians, the rounding of freq / 2 pi, by
+// |p| 2^-65 turns, that of the fraction, and by 2^-33 turns, that of the word.
 //
 // Measured (bf16, replays of a CUDA graph of 20 calls): q and k [8, 2048, 4, 256] channels last to head-major 23 us
 // (5.9 TB/s), half as long again with the angles in 64-bit floating point; q, k [1, 8 + 2, 32768, 128], half of it
@@ -56,7 +57,7 @@ constexpr int kBatch = 2;  // heads loaded together: four leave registers for ha
 
 // Sine and cosine of a 64-bit fraction of a turn.
 __device__ __forceinline__ void sincos_turns(unsigned long long turns, float* sn, float* cs) {
-  const uint32_t w = (uint32_t)(turns >> 32), k = (w + 0x20000000u) >> 30;  // the nearest quadrant
+  const uint32_t w = (uint32_t)((turns + 0x80000000ull) >> 32), k = (w + 0x20000000u) >> 30;  // the nearest quadrant
   const float x = (float)(int)(w - (k << 30)) * 1.4629180792671596e-9f;      // 2 pi / 2^32
   const float y = x * x;
   float s = fmaf(y, 1.f / 362880.f, -1.f / 5040.f), c = fmaf(y, 1.f / 40320.f, -1.f / 720.f);
@@ -73,9 +74,10 @@ __global__ void __launch_bounds__(256, 4) rotary_kernel(const Args a) {
   // The pairs' turns a position as fractions of 2^64.
   extern __shared__ unsigned long long fraction[];  // [R / 2]
   for (int f = threadIdx.x; f < a.R / 2; f += 256) {
-    double turns = a.freq[f] * 0.15915494309189533577;  // 1 / (2 pi)
-    turns -= floor(turns);
-    fraction[f] = __double2ull_rn(turns * 18446744073709551616.0);  // 1.0, if it rounds up to that, becomes 2^64 - 1
+    double turns = fabs(a.freq[f]) * 0.15915494309189533577;  // 1 / (2 pi)
+    turns -= floor(turns);                                    // exact, and below 1
+    const unsigned long long n = __double2ull_rn(turns * 18446744073709551616.0);
+    fraction[f] = __double_as_longlong(a.freq[f]) < 0 ? 0ull - n : n;
   }
   __syncthreads();
   const int h0 = blockIdx.y * a.heads_a_thread, h1 = min(h0 + a.heads_a_thread, a.Hq + a.Hk);

@@ -331,8 +331,9 @@ int gla_group_norm_bwd(const void* x, const void* z, const float* w, const float
  *        position; pos int64: NULL with pos_rows = 0 (p = pos0 + t), [T] with pos_rows = 1 or [B,T]
  *        with pos_rows = B (p = pos0 + pos)
  *   out: qo, ko in `out_layout`; with equal layouts qo = q and ko = k (in place) are allowed
- * The angle is formed and reduced to a turn in 64 bits: it is off by |p freq| 2^-52 radians at most, so
- * far positions keep fp32 accuracy; freq has to be finite.  The rotation is fp32 and rounded once.
+ * The angle is formed and reduced to a turn in 64 bits, and rounded to 32 bits of a turn: it is off by
+ * |p freq| 2^-52 + |p| 2^-62 + 2^-30 radians at most, so far positions keep fp32 accuracy relative to |u| + |v|;
+ * freq has to be finite.  The rotation is fp32 and rounded once.
  * inverse != 0 rotates by -A with the same scale, which is the transpose: the backward of a call is
  * the call with inverse set and the layouts exchanged.  1 <= D <= 8192, R even, 2 <= R <= D; scale
  * finite; B*T and B*T*D/2 at most 2^31 - 512 (else GLA_ERR_UNSUPPORTED).  T == 0 enqueues nothing.
