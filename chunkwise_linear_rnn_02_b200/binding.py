@@ -379,6 +379,11 @@ def _first(t, rank):
     return _dtype_code(t), t.device
 
 
+def _too_long(t):
+    """What to raise for a dimension of 2^31 or more: the library takes 32-bit sizes, and ctypes would drop the rest."""
+    return GLAError(f"every dimension has to be below 2^31, got shape {tuple(t.shape)}")
+
+
 # The current stream's handle without building a Stream object, where this torch has it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
@@ -416,6 +421,8 @@ def scan_fwd(g, x, h0=None, complement: bool = False, output_final_state: bool =
     """
     dt, dev = _first(g, 4)
     B, H, T, D = g.shape
+    if (B | H | T | D) >> 31:
+        raise _too_long(g)
     gp, xp = _operand("g", g, g.dtype, g.shape, dev), _operand("x", x, g.dtype, g.shape, dev)
     hp = _operand("h0", h0, torch.float32, (B, H, D), dev)
     o = torch.empty_like(g)
@@ -429,6 +436,8 @@ def scan_bwd(g, x, do, h0=None, dhT=None, hc=None, complement: bool = False, nee
     """Backward of scan_fwd: returns (dg, dx, dh0 or None).  Without hc the states are recomputed from h0."""
     dt, dev = _first(g, 4)
     B, H, T, D = g.shape
+    if (B | H | T | D) >> 31:
+        raise _too_long(g)
     gp, xp = _operand("g", g, g.dtype, g.shape, dev), _operand("x", x, g.dtype, g.shape, dev)
     dop = _operand("do", do, g.dtype, g.shape, dev)
     hp = _operand("h0", h0, torch.float32, (B, H, D), dev)
@@ -448,6 +457,8 @@ def scan_step(g, x, S, complement: bool = False):
     """One token of scan_fwd: g, x [B,H,D]; S [B,H,D] fp32 updated in place.  Returns o [B,H,D]."""
     dt, dev = _first(g, 3)
     B, H, D = g.shape
+    if (B | H | D) >> 31:
+        raise _too_long(g)
     gp, xp = _operand("g", g, g.dtype, g.shape, dev), _operand("x", x, g.dtype, g.shape, dev)
     if S is None:
         raise GLAError("scan_step needs the state S")
@@ -473,6 +484,8 @@ def _norm_args(x, z, w, b, kind, act, layout):
     dt, dev = _first(x, 4)
     lay = _choice("layout", layout, _LAYOUTS)
     B, H, T, D = x.shape
+    if (B | H | T | D) >> 31:
+        raise _too_long(x)
     if lay:
         H, T = T, H
     out = (B, T, H, D)
@@ -562,6 +575,8 @@ def _rotary(q, k, freq, pos, pos0, interleaved, scale, inverse, in_layout, out_l
     lin, lout = _choice("layout", in_layout, _LAYOUTS), _choice("out_layout", out_layout, _LAYOUTS)
     dtype = q.dtype
     B, Hq, T, D = q.shape
+    if (B | Hq | T | D) >> 31:
+        raise _too_long(q)
     if lin:
         Hq, T = T, Hq
     qp, kp, Hk, ko = _operand("q", q, dtype, q.shape, dev), None, 0, None
@@ -569,9 +584,13 @@ def _rotary(q, k, freq, pos, pos0, interleaved, scale, inverse, in_layout, out_l
         if k.dim() != 4:
             raise GLAError(f"k must have 4 dimensions, got shape {tuple(k.shape)}")
         Hk = k.shape[2 if lin else 1]
+        if Hk >> 31:
+            raise _too_long(k)
         kp = _operand("k", k, dtype, (B, T, Hk, D) if lin else (B, Hk, T, D), dev)
     if freq.dim() != 1:
         raise GLAError(f"freq must be [R/2], got shape {tuple(freq.shape)}")
+    if 2 * freq.shape[0] > D:
+        raise GLAError(f"freq must have at most D/2 = {D // 2} frequencies, got {freq.shape[0]}")
     fp, pp, rows = _operand("freq", freq, torch.float64, freq.shape, dev), None, 0
     if pos is not None:
         one = pos.dim() == 1
