@@ -587,6 +587,8 @@ def _rotary(q, k, freq, pos, pos0, interleaved, scale, inverse, in_layout, out_l
         if Hk >> 31:
             raise _too_long(k)
         kp = _operand("k", k, dtype, (B, T, Hk, D) if lin else (B, Hk, T, D), dev)
+    if not -(1 << 63) <= pos0 < 1 << 63:
+        raise GLAError(f"pos0 has to fit 64 bits, got {pos0}")
     if freq.dim() != 1:
         raise GLAError(f"freq must be [R/2], got shape {tuple(freq.shape)}")
     if 2 * freq.shape[0] > D:

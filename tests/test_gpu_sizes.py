@@ -39,6 +39,13 @@ def test_more_frequencies_than_channels_are_refused():
         gla.rotary(torch.zeros(1, 1, 1, 8, device="cuda"), None, freq)
 
 
+@pytest.mark.parametrize("pos0", [1 << 63, -(1 << 63) - 1, 1 << 70])
+def test_positions_beyond_64_bits_are_refused(pos0):
+    q = torch.zeros(1, 1, 2, 4, device="cuda")
+    with pytest.raises(gla.GLAError, match="pos0"):
+        gla.rotary(q, None, torch.ones(2, dtype=torch.float64, device="cuda"), pos0=pos0)
+
+
 @pytest.mark.parametrize("D", [(1 << 31) - 1, (1 << 31) - 16])
 def test_scan_of_the_widest_rows(D):
     """One token of as many channels as the header allows: the last slab ends where 31 bits end."""
