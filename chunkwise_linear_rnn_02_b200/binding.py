@@ -541,6 +541,7 @@ def rotary_frequencies(R: int, base: float = 10000.0, scaling: str = "none", fac
       "ntk"     base * factor^(R/(R-2)): the slowest pair is interpolated, the fastest left alone
       "yarn"    pairs that turn more than `fast` times over the trained length are left alone, those that turn
                 less than `slow` times are interpolated, a ramp in between; scale = 0.1 ln(factor) + 1
+                ("YaRN: Efficient Context Window Extension of Large Language Models")
     Returns (freq, scale).  Made once for a model; the calls take them as they are.
     """
     if R < 2 or R % 2 or not base > 1 or not factor >= 1:
@@ -563,6 +564,7 @@ def rotary_frequencies(R: int, base: float = 10000.0, scaling: str = "none", fac
 
         lo, hi = max(0, math.floor(pair(fast))), min(R - 1, math.ceil(pair(slow)))
         ramp = ((i / 2 - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        ramp[i / 2 >= hi] = 1.0  # also where hi <= 0: every pair turns less than `slow` times
         freq = freq * (1 - ramp) + freq / factor * ramp
         scale = 0.1 * math.log(factor) + 1.0
     elif scaling not in ("none", "ntk"):
