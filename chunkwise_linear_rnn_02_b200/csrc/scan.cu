@@ -39,6 +39,7 @@
 #include "fused_common.cuh"
 #include "pair_math.cuh"
 #include "scan_cluster.cuh"
+#include "scan_plan.cuh"
 #include "vec.cuh"
 
 namespace {
@@ -54,10 +55,13 @@ using gla::lo;
 using gla::mul2;
 using gla::stf;
 using gla::Two;
+using gla::scan::kByThread;
+using gla::scan::kKeep;
+using gla::scan::kTma;
+using gla::scan::Plan;
 namespace cl = gla::cluster;
 namespace sm = gla::sm100;
 
-constexpr int kKeep = 64;  // tokens between the kept states
 constexpr float kLog2e = gla::fast::kLog2e;
 constexpr double kLn2Exact = 0.693147180559945309417;
 constexpr float kLn2 = (float)kLn2Exact, kLn2Rest = (float)(kLn2Exact - (double)kLn2);
@@ -165,13 +169,6 @@ __device__ __forceinline__ void join_warp(Pair& p, Pair& all, int run) {
     else p = q;
   }
 }
-
-// How a block's tiles come into shared memory (rows of 2 LPR values, one a token):
-//   kTma       one copy of the whole tile by TMA; rows and tensors start on 16 bytes
-//   kByThread  every thread copies what it will read itself, two values or one at a time, asynchronously where they
-//              have 4 bytes at least
-// B=8, T=2048, C=1008 bf16 forward: 20 us by TMA; by thread, C=1002 31 us, C=1001, one value at a time, 44 us.
-enum Load { kTma = 0, kByThread = 1 };
 
 struct Args {
   const void* in[3];   // g, x and, in the backward, dO
@@ -589,87 +586,17 @@ bool make_map(CUtensorMap* m, const void* base, long long BH, int T, int D, int 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// How a variant with slabs of 2 LPR channels is cut: blocks of W warps, MINB of them an SM, R tokens a thread, STAGES
-// tiles in shared memory, up to MAXK blocks a cluster.
-// Blocks of 4 warps: 8 warps with the same bytes in flight pay for joining twice the warps (B=1, T=32768, C=1024 bf16
-// forward a quarter longer).  Forward: 16 tokens a thread at bf16, since 8 make twice the joins an element (B=8, T=2048,
-// C=2048 a fifth longer); one tile of g is 8 KB, so three stages of three blocks fit the 227 KB.  fp32 has 8 tokens for
-// the same 8 KB; on slabs of 64 channels it has 16 and two stages of 16 KB, which serves many channels by TMA (B=8,
-// T=2048, C=2048 65 us, 73 us on slabs of 32) and is too little in flight where the threads copy (C=1002 60 and 39 us).
-// Backward: the third array and the recomputed states take the registers of the other 8 tokens (with 16 the complement
-// spills and takes two and a half times as long), and a tile has to start at a kept state, so slabs of 64 channels
-// would need 8 warps: slabs of 32 are its widest (B=8, T=2048, C=2048 bf16 62 against 65 us).
-template <typename T, int LPR, bool BWD>
-struct Shape {
-  static_assert(!BWD || LPR < 32, "a tile of the backward starts at a kept state");
-  static constexpr int W = 4, MINB = BWD && sizeof(T) == 2 ? 4 : 3;
-  static constexpr int R = BWD || (sizeof(T) == 4 && LPR < 32) ? 8 : 16;
-  static constexpr int STAGES = sizeof(T) == 4 && LPR == 32 ? 2 : 3;
-  static constexpr int MAXK = LPR == 8 ? 16 : LPR == 16 ? 8 : 6;
-};
-
-// How many blocks share a slab, and what that costs.  A step of a block takes a fixed time, more the more blocks
-// exchange, and the work of a tile times the blocks of the SM, which differs with the width of the slab (narrow rows
-// also join across the warp; the complement's backward at bf16 spills on the wider slab):
-//     cost = steps (fixed + block K + work (R / 16) blocks_an_sm)
-// fitted to 54 shapes with every K and slab (both types, 256 to 65,536 tokens, 64 to 6,400 channels in all, rows on
-// 16 bytes, even and odd): what it chooses takes 1.02 times as long as the best choice on average (with one row of
-// constants for all, 1.05 times).
-// K is 1, 2, 3, 4, 6, 8 or 16, all blocks running at once (in between, clusters leave places free: B=1, T=32768, C=1024
-// forward 65 us with 13, 47 us with 8), and clusters of six and more take seven eighths of the places at most, since how
-// they fill the GPU's groups of SMs differs from one GPU to the next (2 x 2 x 3000 x 200 bf16 backward: 16 us with 52
-// clusters of 8, 13 us with 52 of 6; fp32 3 x 2 x 1531 x 333 forward with 66 of 6: 13 us on one GPU, 18 us on another).
-// Clusters of 16 serve where they leave an SM no more than a block.
-struct Cost {
-  double fixed, block, work64, work32, work16;
-};
-template <bool BF16, int LOAD, bool COMP, bool BWD>
-constexpr Cost cost() {
-  if (LOAD == kTma) {
-    if (!BWD) return BF16 ? Cost{0.3, 0.15, 0.6, 0.72, 1.1} : Cost{0.6, 0.08, 0.6, 0.6, 0.9};
-    if (!BF16) return {0.3, 0.11, 0., 0.7, 0.9};
-    return COMP ? Cost{0.6, 0.08, 0., 0.7, 0.69} : Cost{0.6, 0.05, 0., 0.5, 0.75};
-  }
-  if (BF16) return {0.9, 0.08, 0.6, 0.75, BWD ? 1.125 : 1.3};
-  return BWD ? Cost{0.4, 0.08, 0., 0.9, 1.6} : Cost{0.5, 0.08, 0., 0.9, 1.5};
-}
-struct Plan {
-  long long cols = 0;
-  int slabs = 0, tiles = 0, K = 0;
-  double cost = 0.;
-};
-template <typename T, int LPR, int LOAD, bool COMP, bool BWD>
-Plan plan(const Args& a, long long BH) {
-  typedef Shape<T, LPR, BWD> S;
-  typedef Block<T, S::W, LPR, S::R, BWD ? 3 : 2, S::STAGES, S::MAXK, true, LOAD> B;
-  constexpr int SHARED = S::STAGES * B::STAGE + S::W * LPR * (BWD ? 48 : 32) + (int)sizeof(typename B::Ex) + 1088;
-  constexpr int PLACES = 148 * (S::MINB < 233472 / SHARED ? S::MINB : 233472 / SHARED);  // 228 KB an SM
-  constexpr Cost C = cost<sizeof(T) == 2, LOAD, COMP, BWD>();
-  constexpr double work = (LPR == 32 ? C.work64 : LPR == 16 ? C.work32 : C.work16) * S::R / 16;
-  Plan best;
-  best.slabs = (a.D - 1) / B::CW + 1;  // D goes up to 2^31 - 1
-  best.tiles = (int)(((long long)a.T + B::TILE - 1) / B::TILE);
-  best.cols = BH * best.slabs;
-  for (int K : {1, 2, 3, 4, 6, 8, 16}) {
-    const long long n = best.cols * K;
-    if (K > 1 && (K > S::MAXK || K > best.tiles || n > (K < 6 ? PLACES : K < 16 ? PLACES / 8 * 7 : 148))) break;
-    const double c = (double)((best.tiles + K - 1) / K) *
-                     (C.fixed + (K > 1 ? C.block * K : 0.) + work * (double)((n + 147) / 148));
-    if (K == 1 || c < best.cost) best.K = K, best.cost = c;
-  }
-  return best;
-}
-
 template <typename T, int LPR, int LOAD, bool COMP, bool BWD>
 int launch(Args a, const Plan& p, long long BH, cudaStream_t st) {
-  typedef Shape<T, LPR, BWD> S;
+  typedef gla::scan::Shape<sizeof(T) == 2, LPR, BWD> S;
   constexpr int W = S::W, MINB = S::MINB, R = S::R, STAGES = S::STAGES, MAXK = S::MAXK;
   typedef Block<T, W, LPR, R, BWD ? 3 : 2, STAGES, MAXK, true, LOAD> B;
   constexpr int SMEM = STAGES * B::STAGE;
+  static_assert(B::TILE == S::TILE && B::CW == S::CW && B::STAGE == S::STAGE && sizeof(typename B::Ex) == S::EXCHANGE,
+                "the plan counts with what the kernel takes");
   const int K = p.K;
   const long long cols = p.cols;
-  a.slabs = p.slabs, a.tiles = p.tiles, a.K = K;
-  a.steps = (a.tiles + K - 1) / K;
+  a.slabs = p.slabs, a.tiles = p.tiles, a.K = K, a.steps = p.steps;
   Maps maps;
   if (LOAD == kTma && a.T > 0)
     for (int n = 0; n < (BWD ? 3 : 2); ++n)
@@ -711,36 +638,28 @@ int launch(Args a, const Plan& p, long long BH, cudaStream_t st) {
   return GLA_OK;
 }
 
-// Slabs of 64 (forward, but not fp32 copied by the threads), 32 or 16 channels, whichever costs least.
 template <typename T, int LOAD, bool COMP, bool BWD>
-int choose(const Args& a, long long BH, cudaStream_t st) {
-  const Plan mid = plan<T, 16, LOAD, COMP, BWD>(a, BH), narrow = plan<T, 8, LOAD, COMP, BWD>(a, BH);
-  if constexpr (!BWD && (sizeof(T) == 2 || LOAD == kTma)) {
-    const Plan wide = plan<T, 32, LOAD, COMP, BWD>(a, BH);
-    if (wide.cost <= mid.cost && wide.cost <= narrow.cost) return launch<T, 32, LOAD, COMP, BWD>(a, wide, BH, st);
-  }
-  if (mid.cost <= narrow.cost) return launch<T, 16, LOAD, COMP, BWD>(a, mid, BH, st);
-  return launch<T, 8, LOAD, COMP, BWD>(a, narrow, BH, st);
+int launch(const Args& a, long long BH, cudaStream_t st) {
+  const Plan p = gla::scan::choose<sizeof(T) == 2, LOAD, COMP, BWD>(BH, a.T, a.D);
+  if constexpr (!BWD && (sizeof(T) == 2 || LOAD == kTma))
+    if (p.lpr == 32) return launch<T, 32, LOAD, COMP, BWD>(a, p, BH, st);
+  if (p.lpr == 16) return launch<T, 16, LOAD, COMP, BWD>(a, p, BH, st);
+  return launch<T, 8, LOAD, COMP, BWD>(a, p, BH, st);
 }
 
 template <bool BWD>
 int run(Args a, long long BH, int input, int dtype, cudaStream_t st) {
-  const size_t es = esize(dtype);
-  auto fits = [&](size_t bytes) {
-    if (a.D * es % bytes != 0) return false;
-    for (const void* p : {a.in[0], a.in[1], a.in[2], (const void*)a.out0, (const void*)a.out1})
-      if (!gla::aligned_to(p, bytes)) return false;
-    return true;
-  };
-  // TMA counts tokens and heads in 32 bits and strides up to 2^40 bytes.
-  const bool tma = fits(16) && a.T < (1 << 30) && (double)a.D * es * a.T < 1099511627776.0;
-  a.pairs = fits(2 * es);
+  const int es = (int)esize(dtype);
+  uintptr_t at = 0;
+  for (const void* p : {a.in[0], a.in[1], a.in[2], (const void*)a.out0, (const void*)a.out1}) at |= reinterpret_cast<uintptr_t>(p);
+  const bool tma = gla::scan::by_tma(at, a.T, a.D, es);
+  a.pairs = gla::scan::fits(at, a.D, es, 2 * es);
   const bool comp = input == GLA_SCAN_COMPLEMENT;
-#define SCAN_CHOOSE(TYPE)                                                                                             \
-  (tma ? (comp ? choose<TYPE, kTma, true, BWD>(a, BH, st) : choose<TYPE, kTma, false, BWD>(a, BH, st))                \
-       : (comp ? choose<TYPE, kByThread, true, BWD>(a, BH, st) : choose<TYPE, kByThread, false, BWD>(a, BH, st)))
-  return dtype == GLA_DTYPE_BF16 ? SCAN_CHOOSE(bf16) : SCAN_CHOOSE(float);
-#undef SCAN_CHOOSE
+#define SCAN_LAUNCH(TYPE)                                                                                             \
+  (tma ? (comp ? launch<TYPE, kTma, true, BWD>(a, BH, st) : launch<TYPE, kTma, false, BWD>(a, BH, st))                \
+       : (comp ? launch<TYPE, kByThread, true, BWD>(a, BH, st) : launch<TYPE, kByThread, false, BWD>(a, BH, st)))
+  return dtype == GLA_DTYPE_BF16 ? SCAN_LAUNCH(bf16) : SCAN_LAUNCH(float);
+#undef SCAN_LAUNCH
 }
 
 int fwd(const void* g, const void* x, const float* h0, void* o, float* hT, float* hc, int B, int H, int T, int D,
