@@ -5,8 +5,9 @@ using namespace gla::norm;
 
 namespace {
 
-// out[c] = sum over r < rows of part[r][c], always in the same order: 32 groups of 32 threads take every 32nd row of
-// 32 columns, and the groups' sums are added one after another.
+// out[c] = sum over r < rows of part[r][c], always in the same order, and in pairs, so that the rounding grows with the
+// logarithm of the number of rows: 32 groups of 32 threads take every 32nd row of 32 columns, eight of them joined in pairs
+// at a time, and then a warp joins the groups' sums of a column.
 __global__ void __launch_bounds__(1024) join_kernel(const float* part_w, const float* part_b,
                                                     float* __restrict__ dw, float* __restrict__ db, int rows, int cols) {
   // Launched while the kernel before it still runs: nothing is read before that one has ended.
@@ -18,25 +19,23 @@ __global__ void __launch_bounds__(1024) join_kernel(const float* part_w, const f
   const int k = threadIdx.x & 31, g = threadIdx.x >> 5, c = blockIdx.x * 32 + k;
   float t = 0.f;
   if (c < cols) {
-    for (int first = g; first < rows; first += 32 * 8) {  // eight loads in flight: a row's latency is paid once
+#pragma unroll 2
+    for (int first = g; first < rows; first += 32 * 8) {  // sixteen loads in flight: a latency for them all
       float v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int r = first + 32 * i;
         v[i] = r < rows ? part[(size_t)r * cols + c] : 0.f;
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) t += v[i];
+      t += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
     }
   }
   s[g][k] = t;
   __syncthreads();
-  if (g == 0 && c < cols) {
-    t = 0.f;
+  t = s[k][g];  // of the group k, column g
 #pragma unroll
-    for (int i = 0; i < 32; ++i) t += s[i][k];
-    out[c] = t;
-  }
+  for (int d = 1; d < 32; d *= 2) t += __shfl_xor_sync(0xffffffffu, t, d);
+  if (k == 0 && blockIdx.x * 32 + g < cols) out[blockIdx.x * 32 + g] = t;
 }
 
 }  // namespace
