@@ -18,7 +18,10 @@
 // rows in pairs, in a fixed order (no atomics: the result does not depend on how blocks are scheduled).
 //
 // Measured (replays of a CUDA graph of 20 calls) with gate and weights: B=8, H=4, T=2048, D=512 bf16 forward 36 us
-// (5.6 TB/s), backward 68 us (4.9 TB/s); fp32 72 us (5.6 TB/s) and 130 us (5.2 TB/s); B=8, H=4, D=256, one token 2.1 us.
+// (5.7 TB/s), backward 68 us (4.9 TB/s); fp32 72 us (5.6 TB/s) and 133 us (5.0 TB/s); B=8, H=4, D=256, one token 2.0 us.
+// That is at the widths that fill a variant (dispatch, below).  Lanes without a channel issue what the others do, so that D = 80
+// or 640, 62 % of the places, take 1.3 to 1.5 times as long forward and 1.4 to 1.7 times backward for the same bytes; rows off 16
+// bytes have four variants only (bf16 D = 300: 3.5 times as long, D = 1100, a block of 1024 threads a row, 15 times).
 #pragma once
 
 #include <limits.h>
@@ -345,10 +348,11 @@ __global__ void __launch_bounds__(threads_of(LANES), MINB) norm_kernel(const Arg
 }
 
 // ---------------------------------------------------------------------------------------------------- host
-// Threads an SM that the registers allow: 102 to 128 registers a thread at bf16 (16 values a lane), 85 at fp32 (8), 128
-// in the backward.  More threads with fewer registers lose more to spills than they hide: the D = 512 case above takes 45
-// instead of 36 us forward with 768 threads; short rows, which shuffle less, want the registers (H=8, D=64: 8.6 us with
-// 512 threads, 11.6 us with 640).
+// Threads an SM, and so registers a thread: 96 or 128 at bf16 (16 values a lane), 80 at fp32 (8), 128 in the backward.  These leave
+// small spills (nvcc 12.9): 8 to 24 bytes a thread in the gated bf16 backward, 8 or 16 in the gated fp32 forward up to
+// D = 512; blocks of 1024 threads have 64 registers, and their backward spills 16 to 168 bytes.  More threads with fewer registers
+// lose more than they hide: the D = 512 case above takes 45 instead of 36 us forward with 768 threads; short rows, which
+// shuffle less, want the registers (H=8, D=64: 8.6 us with 512 threads, 11.6 us with 640).
 constexpr int resident(int lanes, bool bwd, bool wide) { return bwd ? 512 : wide ? 768 : lanes <= 16 ? 512 : 640; }
 constexpr int blocks_an_sm(int lanes, bool bwd, bool wide) {
   return resident(lanes, bwd, wide) / threads_of(lanes) < 1 ? 1 : resident(lanes, bwd, wide) / threads_of(lanes);

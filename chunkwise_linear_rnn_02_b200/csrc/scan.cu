@@ -2,9 +2,9 @@
 //
 //     h_t = a_t h_{t-1} + b_t,   a_t = exp g_t,   b_t = x_t  or  (1 - a_t) x_t
 //
-// Measured, bf16: B=8, T=2048, C=2048 forward 34 us (5.9 TB/s), backward 62 us (5.4 TB/s), for the complement 39 and
-// 73 us; B=1, T=32768, C=1024 (clusters of eight) forward 47 us, backward 91 us; one token of 32 x 2048 1.5 us.
-// fp32, B=8, T=2048, C=2048: 65 us (6.1 TB/s) and 110 us (6.1 TB/s).
+// Measured, bf16: B=8, T=2048, C=2048 forward 34 us (5.9 TB/s), backward 63 us (5.3 TB/s), for the complement 40 and
+// 72 us; B=1, T=32768, C=1024 (clusters of eight) forward 47 us, backward 91 us; one token of 32 x 2048 1.4 us.
+// fp32, B=8, T=2048, C=2048: 66 us (6.1 TB/s) and 110 us (6.1 TB/s).
 //
 // HBM-bound: g and x are read once and o written once.  A run of tokens acts on the state in front of it as
 // h -> A h + H with A the product of its a's and H its end state from zero, and two runs one after the other
@@ -17,7 +17,8 @@
 // turn.  Each step every block sends its (A, H) to all blocks of the cluster (st.async onto an mbarrier in the
 // receiver's shared memory); every block folds all K of them, in token order, into a carry of its own.  So nothing
 // goes through global memory, nothing waits outside the cluster, whose blocks run together, and the order of all
-// operations is fixed by the sizes.
+// operations is fixed by the sizes, the type and the alignment (which also chooses between TMA and copies by the threads, and
+// so between slabs and clusters: scan_plan.cuh).
 //
 // (All times here and below: replays of a CUDA graph of 20 calls, inputs larger than L2 except where they are small.)
 // What a step costs is instructions (a value has 6 bytes to move at bf16, about 30 issue slots an SM at full

@@ -42,16 +42,21 @@ struct Shape {
 
 // How many blocks share a slab, and what that costs.  A step of a block takes a fixed time, more the more blocks
 // exchange, and the work of a tile times the blocks of the SM, which differs with the width of the slab (narrow rows
-// also join across the warp; the complement's backward at bf16 spills on the wider slab):
+// also join across the warp):
 //     cost = steps (fixed + block K + work (R / 16) blocks_an_sm)
-// fitted to 54 shapes with every K and slab (both types, 256 to 65,536 tokens, 64 to 6,400 channels in all, rows on
-// 16 bytes, even and odd): what it chooses takes 1.02 times as long as the best choice on average (with one row of
-// constants for all, 1.05 times).
+// fitted to 53 shapes with every K and slab (both types, 256 to 65,536 tokens, 64 to 6,400 channels in all, rows on
+// 16 bytes, even and odd): what it chooses takes 1.02 times as long as the best choice within the limits below on average, 1.34
+// times at worst, and 1.05 times as long as the best of all on average, 1.6 times at worst.
+// The complement's backward at bf16 takes the narrow slab at many channels (B=8, T=2048, C=2048: 76 us under the profiler, 85 us
+// on the wide one): it issues 51 instructions a value instead of 48, but has 6.9 blocks an SM instead of 3.5 and waits a
+// quarter as long for loads (long scoreboard 0.3 cycles an issue, 1.3).  Neither spills there; copied by the threads both do,
+// 32 to 40 bytes a thread.
 // K is 1, 2, 3, 4, 6, 8 or 16, all blocks running at once (in between, clusters leave places free: B=1, T=32768, C=1024
 // forward 65 us with 13, 47 us with 8), and clusters of six and more take seven eighths of the places at most, since how
 // they fill the GPU's groups of SMs differs from one GPU to the next (2 x 2 x 3000 x 200 bf16 backward: 16 us with 52
 // clusters of 8, 13 us with 52 of 6; fp32 3 x 2 x 1531 x 333 forward with 66 of 6: 13 us on one GPU, 18 us on another).
-// Clusters of 16 serve where they leave an SM no more than a block.
+// Clusters of 16 serve where they leave an SM no more than a block (on a GPU that took more of them, 2 x 20000 x 96 bf16 backward
+// had 22 us with 192 blocks, 31 us with the clusters of 8 that this rule leaves).
 struct Cost {
   double fixed, block, work64, work32, work16;
 };
