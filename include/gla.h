@@ -277,8 +277,8 @@ int gla_msgla_hold_bwd(const void* dout, void* dy, int B, int H, int T, int D, i
  * operators need the alignment of their element type only; 16-byte aligned ones with rows of a
  * multiple of 16 bytes run the vector form.  Results do not depend on the number of SMs or on the
  * order in which blocks run; a tensor off its alignment may give other last bits than an aligned copy.
- * At fp32 a and 1 - a are off by a few 2^-24 of themselves for every g; at bf16 a by 2^-22 + |g| 2^-24
- * and 1 - a by 2^-20.7.
+ * At fp32 a and 1 - a are off by a few 2^-24 of themselves for every g (an a below 2^-126 is zero); at bf16
+ * a by 2^-22 + |g| 2^-24 and 1 - a by 2^-20.7.
  * ------------------------------------------------------------------------------------- */
 typedef enum { GLA_SCAN_ADD = 0, GLA_SCAN_COMPLEMENT = 1 } gla_scan_input;
 
