@@ -338,7 +338,7 @@ int gla_group_norm_bwd(const void* x, const void* z, const float* w, const float
  * freq has to be finite.  The rotation is fp32 and rounded once.
  * inverse != 0 rotates by -A with the same scale, which is the transpose: the backward of a call is
  * the call with inverse set and the layouts exchanged.  1 <= D <= 8192, R even, 2 <= R <= D; scale
- * finite; B*T and B*T*D/2 at most 2^31 - 512 (else GLA_ERR_UNSUPPORTED).  T == 0 enqueues nothing.
+ * finite; B*T and B*T*ceil(D/2) at most 2^31 - 512 (else GLA_ERR_UNSUPPORTED).  T == 0 enqueues nothing.
  * ------------------------------------------------------------------------------------- */
 int gla_rotary(const void* q, const void* k, void* qo, void* ko, const double* freq, const long long* pos,
                long long pos0, int pos_rows, int B, int Hq, int Hk, int T, int D, int R, float scale,
